@@ -450,6 +450,88 @@ mla_status mla_prefill_attn(const mla_bf16* q_nope, const mla_bf16* q_rope, cons
                             cudaStream_t stream);
 
 /*
+ * The layer in few bits: the norms between the projections, projections with
+ * 4-bit weights, and the FP8 cache read back for the non-absorbed path.
+ * ("DeepSeek-MLA-Principle" section 7 names mixed precision with scaling; the
+ * pages give no weight or activation format, and their listing has no norms:
+ * formats and placement are this library's, stated below.)
+ *
+ * mla_rms_norm -- root-mean-square norm of T rows, with the residual's addition
+ * before it and a bf16 and/or an 8-bit output:
+ *   h = x + residual (h = x without one); residual_out = bf16(h)
+ *   v = h / sqrt(mean(h^2) + eps) * weight
+ *   y = bf16(v)
+ *   y_scale[t, g] = s = max(max|v| / 448, 2^-100) over columns [128 g, 128 g + 128)
+ *   y8 = E4M3(v / s), nearest even
+ * h, its sum of squares and v are float32 (h is not rounded before the norm).
+ *   x            [T, D] bf16, row t at x + t * x_ld (x_ld >= D, a multiple of 8)
+ *   residual     [T, D] bf16 (nullable, with residual_out)
+ *   residual_out [T, D] bf16 out; may be `residual` itself
+ *   weight       [D] bf16
+ *   y            [T, D] bf16 out (nullable); may be x itself when x_ld = D
+ *   y8, y_scale  [T, D] uint8 codes and [T, ceil(D / 128)] float32 out (nullable, both or neither)
+ * T >= 0; D a multiple of 8, 8 .. MLA_NORM_MAX_D (MLA_ERR_UNSUPPORTED beyond).
+ * At least one output form; eps >= 0; no other overlap between inputs and
+ * outputs than the two named (MLA_ERR_INVALID_ARG).  A row that holds a NaN is NaN
+ * throughout, one that holds an infinity is NaN there and 0 elsewhere; a NaN's
+ * code in y8 is 0x7F or 0xFF, and it does not enter its group's maximum.
+ */
+#define MLA_NORM_MAX_D 16384
+mla_status mla_rms_norm(const mla_bf16* x, int64_t x_ld, const mla_bf16* residual, mla_bf16* residual_out,
+                        const mla_bf16* weight, float eps, mla_bf16* y, uint8_t* y8, float* y_scale,
+                        int T, int D, cudaStream_t stream);
+
+/*
+ * 4-bit weights.  A row of K weights is K / 2 bytes, column 2i in the low half
+ * of byte i and column 2i + 1 in the high half; a half byte u stands for
+ * (u - 8) * s, with one bf16 scale s for each 128 columns (MLA_W4_GROUP) of the
+ * row, the last group shorter when K is no multiple of 128.
+ *   w4      [N, K / 2] uint8
+ *   w_scale [N, ceil(K / 128)] bf16
+ *
+ * mla_quantize_w4 -- that form of w [N, K] bf16 (finite): s = bf16(max|w| / 7),
+ *   or 1 where that is zero; u = clamp(round(w / s), -8, 7) + 8, nearest even.
+ *   IEEE operations throughout: the same codes on every run.
+ * mla_dequantize_w4 -- w [N, K] bf16 out: bf16((u - 8) * s).
+ * mla_linear_w4 -- y[t][n] = bf16(sum_k x[t][k] (u[n][k] - 8) s[n][k / 128]): mla_linear
+ *   with such weights.  x [T, K] bf16, y [T, N] bf16 out, 1 <= T <= MLA_LINEAR_MAX_T.
+ * mla_linear_w4_fp8 -- the same with 8-bit x as mla_rms_norm writes it: x8 [T, K]
+ *   E4M3 codes, x_scale [T, ceil(K / 128)] float32, x = E4M3(x8) * x_scale.
+ * The products u - 8 times x are exact and summed in float32, the scales are
+ * applied to each group's sum in float32, and y is rounded once.  K is split
+ * over the CTAs of a cluster, whose partials are added in a fixed order on
+ * chip: no workspace, and a result that does not depend on timing.
+ * N >= 1, K >= 64 a multiple of 64; y must not overlap an input.
+ */
+#define MLA_W4_GROUP 128
+mla_status mla_quantize_w4(const mla_bf16* w, uint8_t* w4, mla_bf16* w_scale, int N, int K, cudaStream_t stream);
+mla_status mla_dequantize_w4(const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* w, int N, int K,
+                             cudaStream_t stream);
+mla_status mla_linear_w4(const mla_bf16* x, const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* y,
+                         int T, int K, int N, cudaStream_t stream);
+mla_status mla_linear_w4_fp8(const uint8_t* x8, const float* x_scale, const uint8_t* w4, const mla_bf16* w_scale,
+                             mla_bf16* y, int T, int K, int N, cudaStream_t stream);
+
+/*
+ * mla_read_kv_fp8 -- the FP8 latent cache read back into bf16 rows, so that the
+ * non-absorbed path (mla_decompress_kv, mla_prefill_attn) can follow
+ * mla_append_kv_fp8: row t of sequence b is [bf16(s E4M3(code)) ; bf16(s f16(key))].
+ *   cache_c8, cache_scale, cache_kr, num_pages, page_table, pt_stride: as for
+ *              mla_append_kv_fp8
+ *   kv_lens    [B] int32 tokens to read per sequence, 0 .. max_kv_len
+ *   rows       [B * P, 64, 576] bf16 out, P = ceil(max_kv_len / 64): token t of
+ *              sequence b at page b * P + t / 64, slot t % 64, i.e. a paged cache
+ *              whose page table is b * P + 0 .. P - 1.  Rows at and past
+ *              kv_lens[b] are left as they were.
+ * pt_stride >= P; B <= 65535 (MLA_ERR_UNSUPPORTED beyond).  A length outside
+ * its range (that sequence) or a page id out of range (that page) is skipped
+ * and sets MLA_ERR_BOUNDS in the device status.
+ */
+mla_status mla_read_kv_fp8(const uint8_t* cache_c8, const float* cache_scale, const uint16_t* cache_kr,
+                           int64_t num_pages, const int32_t* page_table, int pt_stride, const int32_t* kv_lens,
+                           int B, int max_kv_len, mla_bf16* rows, cudaStream_t stream);
+
+/*
  * mla_selftest_wait_timeout -- exercises the failure path of the bounded waits
  * every kernel uses (no counterpart on the MLA pages).  One warp waits on an
  * mbarrier that nothing completes; after limit_ns nanoseconds (1 .. 2e9) of

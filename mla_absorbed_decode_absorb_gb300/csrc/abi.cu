@@ -49,6 +49,45 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 mla_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
+// A tensor's bytes; an absent one overlaps nothing.
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  if (a.p == nullptr || b.p == nullptr) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+Range w4_range(const uint8_t* w4, int N, int K) { return {w4, static_cast<size_t>(N) * (K / 2)}; }
+Range w4_scale_range(const mla_bf16* s, int N, int K) {
+  return {s, static_cast<size_t>(N) * ((K + MLA_W4_GROUP - 1) / MLA_W4_GROUP) * 2};
+}
+
+// The checks every 4-bit-weight call shares.
+mla_status w4_check(const uint8_t* w4, const mla_bf16* w_scale, int N, int K) {
+  if (N < 1 || K < 64 || K % 64 != 0 || !w4 || !w_scale || !aligned16(w4) || !aligned16(w_scale))
+    return MLA_ERR_INVALID_ARG;
+  // a weight's groups are counted in 32 bits
+  if (static_cast<int64_t>(N) * ((K + MLA_W4_GROUP - 1) / MLA_W4_GROUP) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+mla_status linear_w4_check(const void* x, int x_elem, const float* x_scale, const uint8_t* w4,
+                           const mla_bf16* w_scale, const mla_bf16* y, int T, int K, int N) {
+  if (T < 1 || T > MLA_LINEAR_MAX_T) return MLA_ERR_INVALID_ARG;
+  const mla_status s = w4_check(w4, w_scale, N, K);
+  if (s != MLA_OK) return s;
+  if (!x || !y || !aligned16(x) || (reinterpret_cast<uintptr_t>(y) & 1u) != 0) return MLA_ERR_INVALID_ARG;
+  const Range out{y, static_cast<size_t>(T) * N * 2};
+  const size_t groups = (static_cast<size_t>(K) + MLA_W4_GROUP - 1) / MLA_W4_GROUP;
+  if (overlap(out, {x, static_cast<size_t>(T) * K * x_elem}) || overlap(out, {x_scale, T * groups * sizeof(float)}) ||
+      overlap(out, w4_range(w4, N, K)) || overlap(out, w4_scale_range(w_scale, N, K)))
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // The device address of [p, p + bytes) if the current device can address all of
@@ -286,6 +325,85 @@ mla_status mla_linear_pair(const mla_bf16* x, int T, int K, const mla_bf16* w0, 
   int* st = status_ptr();
   if (st == nullptr) return MLA_ERR_CUDA;
   return from_cuda(launch_linear_pair(x, w0, y0, N0, w1, y1, N1, T, K, static_cast<float*>(workspace), st, stream));
+}
+
+mla_status mla_rms_norm(const mla_bf16* x, int64_t x_ld, const mla_bf16* residual, mla_bf16* residual_out,
+                        const mla_bf16* weight, float eps, mla_bf16* y, uint8_t* y8, float* y_scale,
+                        int T, int D, cudaStream_t stream) {
+  if (T < 0 || D < 8 || D % 8 != 0 || x_ld < D || x_ld % 8 != 0 || !(eps >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (D > MLA_NORM_MAX_D) return MLA_ERR_UNSUPPORTED;
+  if (T == 0) return MLA_OK;
+  if ((residual == nullptr) != (residual_out == nullptr) || (y8 == nullptr) != (y_scale == nullptr) ||
+      (y == nullptr && y8 == nullptr))
+    return MLA_ERR_INVALID_ARG;
+  if (!x || !weight) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(weight) || !aligned16(y) ||
+      !aligned16(y8) || !aligned16(y_scale))
+    return MLA_ERR_INVALID_ARG;
+  const size_t row = static_cast<size_t>(D) * 2, all = row * T, codes = all / 2;
+  const size_t scales = static_cast<size_t>(T) * ((D + 127) / 128) * sizeof(float);
+  const size_t x_bytes = static_cast<size_t>(x_ld) * 2 * (T - 1) + row;
+  const Range in[] = {{x, x_bytes}, {residual, all}, {weight, row}};
+  const Range out[] = {{residual_out, all}, {y, all}, {y8, codes}, {y_scale, scales}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      const bool in_place = (o == 0 && i == 1 && residual_out == residual) || (o == 1 && i == 0 && y == x && x_ld == D);
+      if (!in_place && overlap(out[o], in[i])) return MLA_ERR_INVALID_ARG;
+    }
+    for (int q = 0; q < o; ++q)
+      if (overlap(out[o], out[q])) return MLA_ERR_INVALID_ARG;
+  }
+  return from_cuda(launch_rms_norm(x, x_ld, residual, residual_out, weight, eps, y, y8, y_scale, T, D, stream));
+}
+
+mla_status mla_quantize_w4(const mla_bf16* w, uint8_t* w4, mla_bf16* w_scale, int N, int K, cudaStream_t stream) {
+  const mla_status s = w4_check(w4, w_scale, N, K);
+  if (s != MLA_OK) return s;
+  if (!w || !aligned16(w)) return MLA_ERR_INVALID_ARG;
+  const Range in{w, static_cast<size_t>(N) * K * 2};
+  if (overlap(in, w4_range(w4, N, K)) || overlap(in, w4_scale_range(w_scale, N, K)) ||
+      overlap(w4_range(w4, N, K), w4_scale_range(w_scale, N, K)))
+    return MLA_ERR_INVALID_ARG;
+  return from_cuda(launch_quantize_w4(w, w4, w_scale, N, K, stream));
+}
+
+mla_status mla_dequantize_w4(const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* w, int N, int K,
+                             cudaStream_t stream) {
+  const mla_status s = w4_check(w4, w_scale, N, K);
+  if (s != MLA_OK) return s;
+  if (!w || !aligned16(w)) return MLA_ERR_INVALID_ARG;
+  const Range out{w, static_cast<size_t>(N) * K * 2};
+  if (overlap(out, w4_range(w4, N, K)) || overlap(out, w4_scale_range(w_scale, N, K))) return MLA_ERR_INVALID_ARG;
+  return from_cuda(launch_dequantize_w4(w4, w_scale, w, N, K, stream));
+}
+
+mla_status mla_linear_w4(const mla_bf16* x, const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* y, int T, int K,
+                         int N, cudaStream_t stream) {
+  const mla_status s = linear_w4_check(x, 2, nullptr, w4, w_scale, y, T, K, N);
+  return s != MLA_OK ? s : from_cuda(launch_linear_w4(x, nullptr, w4, w_scale, y, T, K, N, stream));
+}
+
+mla_status mla_linear_w4_fp8(const uint8_t* x8, const float* x_scale, const uint8_t* w4, const mla_bf16* w_scale,
+                             mla_bf16* y, int T, int K, int N, cudaStream_t stream) {
+  if (!x_scale || !aligned16(x_scale)) return MLA_ERR_INVALID_ARG;
+  const mla_status s = linear_w4_check(x8, 1, x_scale, w4, w_scale, y, T, K, N);
+  return s != MLA_OK ? s : from_cuda(launch_linear_w4(x8, x_scale, w4, w_scale, y, T, K, N, stream));
+}
+
+mla_status mla_read_kv_fp8(const uint8_t* cache_c8, const float* cache_scale, const uint16_t* cache_kr,
+                           int64_t num_pages, const int32_t* page_table, int pt_stride, const int32_t* kv_lens,
+                           int B, int max_kv_len, mla_bf16* rows, cudaStream_t stream) {
+  if (B < 0 || max_kv_len < 0 || num_pages < 0 || pt_stride < 0) return MLA_ERR_INVALID_ARG;
+  if (B > 65535) return MLA_ERR_UNSUPPORTED;  // one grid row per sequence
+  if (B == 0 || max_kv_len == 0) return MLA_OK;
+  if (!cache_c8 || !cache_scale || !cache_kr || !page_table || !kv_lens || !rows) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(cache_c8) || !aligned16(cache_scale) || !aligned16(cache_kr) || !aligned16(rows))
+    return MLA_ERR_INVALID_ARG;
+  if (pt_stride < (max_kv_len - 1) / kPage + 1) return MLA_ERR_INVALID_ARG;
+  int* st = status_ptr();
+  if (st == nullptr) return MLA_ERR_CUDA;
+  return from_cuda(launch_read_kv_fp8(cache_c8, cache_scale, cache_kr, num_pages, page_table, pt_stride, kv_lens, B,
+                                      max_kv_len, rows, st, stream));
 }
 
 mla_status mla_rope_q(const mla_bf16* q_rope, const int32_t* seq_lens_before, const float* rope_table,

@@ -176,6 +176,19 @@ cudaError_t launch_rope_q(const uint16_t* q_rope, const int32_t* seq_lens_before
                           int rope_max_pos, uint16_t* q_abs, int B, int n_q, int* status, cudaStream_t stream);
 cudaError_t launch_f32_to_bf16(const float* src, uint16_t* dst, int64_t n, cudaStream_t stream);
 
+cudaError_t launch_rms_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual, uint16_t* residual_out,
+                            const uint16_t* w, float eps, uint16_t* y, uint8_t* y8, float* y8_scale, int T, int D,
+                            cudaStream_t stream);
+cudaError_t launch_quantize_w4(const uint16_t* w, uint8_t* w4, uint16_t* scale, int N, int K, cudaStream_t stream);
+cudaError_t launch_dequantize_w4(const uint8_t* w4, const uint16_t* scale, uint16_t* w, int N, int K,
+                                 cudaStream_t stream);
+// x: bf16 with x_scale == nullptr, else E4M3 codes
+cudaError_t launch_linear_w4(const void* x, const float* x_scale, const uint8_t* w4, const uint16_t* w_scale,
+                             uint16_t* y, int T, int K, int N, cudaStream_t stream);
+cudaError_t launch_read_kv_fp8(const uint8_t* c8, const float* scale, const uint16_t* kr, int64_t num_pages,
+                               const int32_t* page_table, int pt_stride, const int32_t* kv_lens, int B,
+                               int max_kv_len, uint16_t* rows, int* status, cudaStream_t stream);
+
 // o_part: the bf16 partials of launch_decode_partial
 cudaError_t launch_combine(const uint16_t* o_part, const float* lse_part, int B, int n_q,
                            int num_splits, float* o_latent, float* lse, cudaStream_t stream);

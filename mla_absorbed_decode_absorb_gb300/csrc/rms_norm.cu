@@ -1,0 +1,146 @@
+// Root-mean-square norm of [T, D] rows, with the residual's addition before it
+// and a bf16 or an 8-bit output:
+//
+//   h = x + r            r_out = bf16(h)
+//   y = h / sqrt(mean(h^2) + eps) * w
+//   y_out = bf16(y)      or, for each 128 columns, s = max(max|y| / 448, 2^-100)
+//                        and codes E4M3(y / s)
+//
+// One CTA owns one row and keeps it in registers between the two sweeps the
+// formula needs (the sum of squares, then the scaling), so x and r are read
+// once.  The sum, h and y stay in fp32: y comes from the unrounded h, and each
+// output is rounded once.  A group of 128 columns is 16 neighbouring lanes of 8
+// columns each, so its maximum is four shuffles.
+#include "append_row.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
+
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* r;      // nullptr: no residual
+  const uint16_t* w;
+  uint16_t* r_out;
+  uint16_t* y;            // bf16 output, or nullptr
+  uint8_t* y8;            // 8-bit output, or nullptr
+  float* s8;
+  int64_t x_ld;
+  int D, groups;
+  float eps;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// kChunks chunks of 8 columns per thread: chunk i of a thread is threadIdx.x +
+// i * blockDim.x, and blockDim.x is a multiple of 32, so 16 neighbouring lanes
+// always hold one whole group of 128 columns.
+template <int kChunks>
+__global__ void __launch_bounds__(kMaxThreads)
+rms_norm_kernel(const NormParams p) {
+  __shared__ float warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x;
+  const int chunks = p.D >> 3;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.x_ld);
+  const int64_t base = row * chunks;
+  uint4 xv[kChunks], rv[kChunks], wv[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = tid + i * static_cast<int>(blockDim.x);
+    xv[i] = rv[i] = wv[i] = make_uint4(0, 0, 0, 0);
+    if (c < chunks) {
+      xv[i] = x[c];
+      if (p.r != nullptr) rv[i] = reinterpret_cast<const uint4*>(p.r)[base + c];
+      wv[i] = reinterpret_cast<const uint4*>(p.w)[c];
+    }
+  }
+  float h[kChunks][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    unpack8(xv[i], h[i]);
+    if (p.r != nullptr) {
+      float r[8];
+      unpack8(rv[i], r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] += r[e];
+      const int c = tid + i * static_cast<int>(blockDim.x);
+      if (c < chunks) reinterpret_cast<uint4*>(p.r_out)[base + c] = pack8(h[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(h[i][e], h[i][e], sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) warp_sum[warp] = sum;
+  __syncthreads();
+  // every warp adds the warps' sums in the same order
+  const int warps = blockDim.x >> 5;
+  sum = lane < warps ? warp_sum[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(p.D)) + p.eps));
+
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = tid + i * static_cast<int>(blockDim.x);
+    float w[8];
+    unpack8(wv[i], w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * inv * w[e];
+    if (p.y != nullptr && c < chunks) reinterpret_cast<uint4*>(p.y)[base + c] = pack8(h[i]);
+    if (p.y8 != nullptr) {
+      float a = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(h[i][e]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      const float s = fmaxf(__fdiv_rn(a, 448.f), kScaleFloor);
+      uint16_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = e4m3x2(__fdiv_rn(h[i][2 * e], s), __fdiv_rn(h[i][2 * e + 1], s));
+      if (c < chunks) {
+        reinterpret_cast<uint2*>(p.y8)[base + c] =
+            make_uint2(q[0] | (static_cast<uint32_t>(q[1]) << 16), q[2] | (static_cast<uint32_t>(q[3]) << 16));
+        if ((c & 15) == 0) p.s8[row * p.groups + (c >> 4)] = s;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual, uint16_t* residual_out,
+                            const uint16_t* w, float eps, uint16_t* y, uint8_t* y8, float* y8_scale, int T, int D,
+                            cudaStream_t stream) {
+  const NormParams p{x, residual, w, residual_out, y, y8, y8_scale, x_ld, D, (D + 127) / 128, eps};
+  const int chunks = D >> 3;
+  auto threads = [&](int per) { return dim3(((chunks + per - 1) / per + 31) / 32 * 32); };
+  if (chunks <= kMaxThreads) return launch_kernel(rms_norm_kernel<1>, dim3(T), threads(1), 0, stream, p);
+  return launch_kernel(rms_norm_kernel<2>, dim3(T), threads(2), 0, stream, p);
+}
+
+}  // namespace mla

@@ -1,0 +1,26 @@
+// The 4-bit weight format and its conversions to bf16 pairs.
+//
+// A weight row of K values is K / 2 bytes, column 2i in the low half of byte i
+// and column 2i + 1 in the high half; a half byte u stands for (u - 8) * s with
+// one bf16 scale s for each 128 columns.
+#pragma once
+
+#include "internal.cuh"
+
+namespace mla {
+
+constexpr int kW4Group = MLA_W4_GROUP;
+__host__ __device__ inline int w4_groups(int K) { return (K + kW4Group - 1) / kW4Group; }
+
+// The eight half bytes u_0 .. u_7 of a word as four bf16 pairs (u_i - 8, u_{i+4} - 8),
+// i = 0 .. 3: 0x4300 is 128, whose bf16 unit in the last place is 1, so 0x4300 | u
+// is 128 + u, and the difference to 136 is exact.
+__device__ __forceinline__ void w4_pairs(uint32_t v, uint32_t (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t biased = ((v >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(biased), "r"(0x43084308u));
+  }
+}
+
+}  // namespace mla

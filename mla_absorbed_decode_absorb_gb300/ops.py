@@ -15,7 +15,7 @@ import os
 
 import torch
 
-from .workloads import D_LATENT, D_NOPE, D_ROPE, D_ROW, N_HEADS
+from .workloads import D_LATENT, D_NOPE, D_ROPE, D_ROW, N_HEADS, empty_cache
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla_decode.so")
@@ -61,6 +61,12 @@ _SIGS = {
     "mla_linear_pair_workspace_size": ([_i, _i, _i, _i, ctypes.POINTER(_sz)], _i),
     "mla_linear_pair": ([_p, _i, _i, _p, _i, _p, _p, _i, _p, _p, _sz, _p], _i),
     "mla_linear_strided": ([_p, _p, _p, _i, _i, _i, _i64, _i, _i, _p, _sz, _p], _i),
+    "mla_rms_norm": ([_p, _i64, _p, _p, _p, ctypes.c_float, _p, _p, _p, _i, _i, _p], _i),
+    "mla_quantize_w4": ([_p, _p, _p, _i, _i, _p], _i),
+    "mla_dequantize_w4": ([_p, _p, _p, _i, _i, _p], _i),
+    "mla_linear_w4": ([_p, _p, _p, _p, _i, _i, _i, _p], _i),
+    "mla_linear_w4_fp8": ([_p, _p, _p, _p, _p, _i, _i, _i, _p], _i),
+    "mla_read_kv_fp8": ([_p, _p, _p, _i64, _p, _i, _p, _i, _i, _p, _p], _i),
     "mla_rope_q": ([_p, _p, _p, _i, _p, _i, _i, _p], _i),
     "mla_f32_to_bf16": ([_p, _p, _i64, _p], _i),
     "mla_append_kv_fp8": ([_p, _p, _p, _p, _i, _p, _i, _p, _p, _p, _i64, _i, _i, _p], _i),
@@ -233,6 +239,147 @@ def mla_linear_strided(x, w, y, y_ld, seg, seg_ld, workspace=None, stream=None):
         0 if not need else _dev(workspace, "workspace", torch.uint8), 0 if not need else workspace.numel(),
         _stream(stream)))
     return y
+
+
+W4_GROUP = 128  # columns that share a scale, in 4-bit weights and in 8-bit activations (MLA_W4_GROUP)
+
+
+def _groups(n: int) -> int:
+    return (n + W4_GROUP - 1) // W4_GROUP
+
+
+def _on_current_device(first: torch.Tensor, *others):
+    """The kernels run on the current device: tensors of another one are refused."""
+    for t in (first, *others):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("expected a torch.Tensor")
+        if t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream):
+    if x.dim() != 2:
+        raise ValueError("x must be [T, D]")
+    T, D = x.shape
+    if not x.is_cuda or x.dtype != torch.bfloat16:
+        raise TypeError("x must be a CUDA bf16 tensor")
+    if D > 1 and x.stride(1) != 1:
+        raise ValueError("x's columns must be contiguous")
+    x_ld = x.stride(0) if T > 1 else max(D, 8)
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without residual")
+    _on_current_device(x, weight, residual, residual_out, y, y8, y_scale)
+    _check("mla_rms_norm", lib.mla_rms_norm(
+        x.data_ptr(), int(x_ld),
+        0 if residual is None else _dev(residual, "residual", torch.bfloat16, (T, D)),
+        0 if residual is None else _dev(residual_out, "residual_out", torch.bfloat16, (T, D)),
+        _dev(weight, "weight", torch.bfloat16, (D,)), float(eps),
+        0 if y is None else _dev(y, "y", torch.bfloat16, (T, D)),
+        0 if y8 is None else _dev(y8, "y8", torch.uint8, (T, D)),
+        0 if y_scale is None else _dev(y_scale, "y_scale", torch.float32, (T, _groups(D))),
+        int(T), int(D), _stream(stream)))
+
+
+def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, stream=None):
+    """``y = h / sqrt(mean(h^2) + eps) * weight`` with ``h = x + residual``, in bf16.
+
+    x [T, D] may have a row stride (a multiple of 8); with ``residual`` the sum h is written to
+    ``residual_out`` (default: in place)."""
+    if y is None:
+        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    _rms_norm(x, weight, eps, residual, residual_out, y, None, None, stream)
+    return y
+
+
+def mla_rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y8=None, y_scale=None, y=None,
+                     stream=None):
+    """:func:`mla_rms_norm` with an 8-bit output: (E4M3 codes [T, D] uint8, scales [T, ceil(D/128)] float32),
+    what ``mla_linear_w4_fp8`` reads.  With ``y`` the bf16 output is written too."""
+    if y8 is None:
+        y8 = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    if y_scale is None:
+        y_scale = torch.empty(x.shape[0], _groups(x.shape[-1]), dtype=torch.float32, device=x.device)
+    _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream)
+    return y8, y_scale
+
+
+def mla_quantize_w4(w, w4=None, w_scale=None, stream=None):
+    """4-bit weights of ``w [N, K]`` bf16: (half bytes [N, K/2] uint8, scales [N, ceil(K/128)] bf16)."""
+    N, K = w.shape
+    if w4 is None:
+        w4 = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device)
+    if w_scale is None:
+        w_scale = torch.empty(N, _groups(K), dtype=torch.bfloat16, device=w.device)
+    _on_current_device(w, w4, w_scale)
+    _check("mla_quantize_w4", lib.mla_quantize_w4(
+        _dev(w, "w", torch.bfloat16), _dev(w4, "w4", torch.uint8, (N, K // 2)),
+        _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))), int(N), int(K), _stream(stream)))
+    return w4, w_scale
+
+
+def mla_dequantize_w4(w4, w_scale, w=None, stream=None):
+    """``w [N, K]`` bf16 of 4-bit weights."""
+    N, K = w4.shape[0], 2 * w4.shape[1]
+    if w is None:
+        w = torch.empty(N, K, dtype=torch.bfloat16, device=w4.device)
+    _on_current_device(w4, w_scale, w)
+    _check("mla_dequantize_w4", lib.mla_dequantize_w4(
+        _dev(w4, "w4", torch.uint8, (N, K // 2)), _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))),
+        _dev(w, "w", torch.bfloat16, (N, K)), int(N), int(K), _stream(stream)))
+    return w
+
+
+def mla_linear_w4(x, w4, w_scale, y=None, stream=None):
+    """``y [T, N] = x [T, K] w^T`` in bf16 with 4-bit weights (fp32 accumulation, no workspace)."""
+    T, K = x.shape
+    N = w4.shape[0]
+    if y is None:
+        y = torch.empty(T, N, dtype=torch.bfloat16, device=x.device)
+    _on_current_device(x, w4, w_scale, y)
+    _check("mla_linear_w4", lib.mla_linear_w4(
+        _dev(x, "x", torch.bfloat16, (T, K)), _dev(w4, "w4", torch.uint8, (N, K // 2)),
+        _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))), _dev(y, "y", torch.bfloat16, (T, N)),
+        int(T), int(K), int(N), _stream(stream)))
+    return y
+
+
+def mla_linear_w4_fp8(x8, x_scale, w4, w_scale, y=None, stream=None):
+    """:func:`mla_linear_w4` of 8-bit activations as :func:`mla_rms_norm_fp8` returns them."""
+    T, K = x8.shape
+    N = w4.shape[0]
+    if y is None:
+        y = torch.empty(T, N, dtype=torch.bfloat16, device=x8.device)
+    _on_current_device(x8, x_scale, w4, w_scale, y)
+    _check("mla_linear_w4_fp8", lib.mla_linear_w4_fp8(
+        _dev(x8, "x8", torch.uint8, (T, K)), _dev(x_scale, "x_scale", torch.float32, (T, _groups(K))),
+        _dev(w4, "w4", torch.uint8, (N, K // 2)), _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))),
+        _dev(y, "y", torch.bfloat16, (T, N)), int(T), int(K), int(N), _stream(stream)))
+    return y
+
+
+def mla_read_kv_fp8(cache_fp8, page_table, kv_lens, max_kv_len, rows=None, stream=None):
+    """The FP8 cache read back as bf16 rows ``[B * P, 64, 576]``, P = ceil(max_kv_len / 64): a paged cache whose
+    page table is ``arange(B * P).view(B, P)``.  Rows past a sequence's length are left as they were (rows
+    allocated here are NaN there, as in an empty cache)."""
+    c8, scale, kr = cache_fp8
+    B, P = int(kv_lens.shape[0]), int(c8.shape[0])
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    shape = (B * ((int(max_kv_len) + 63) // 64), 64, D_ROW)
+    if rows is None:
+        rows = empty_cache(shape[0], c8.device)
+    _on_current_device(c8, scale, kr, page_table, kv_lens, rows)
+    _check("mla_read_kv_fp8", lib.mla_read_kv_fp8(
+        _dev(c8, "cache_c8", torch.uint8, (P, 64, D_LATENT)), _dev(scale, "cache_scale", torch.float32, (P, 64)),
+        _dev(kr, "cache_kr", torch.float16, (P, 64, D_ROPE)), P,
+        _dev(page_table, "page_table", torch.int32), int(page_table.shape[1]),
+        _dev(kv_lens, "kv_lens", torch.int32, (B,)), int(B), int(max_kv_len),
+        _dev(rows, "rows", torch.bfloat16, shape), _stream(stream)))
+    return rows
 
 
 def mla_rope_q(q_rope, seq_lens_before, rope, q_abs, stream=None):
