@@ -11,18 +11,23 @@
 //
 // A few tokens leave the work at streaming W once: half a byte per weight.
 // Weights are the 16-row side of the warp MMA (m16n8k16), tokens the 8-column
-// side.  A thread's share of one group of a 16-row tile is 16 bytes of row g and
-// 16 of row g + 8 (g = lane / 4), 32 consecutive columns each, fetched by its own
-// cp.async ring: no thread reads another's bytes, so the stream needs no
-// barrier.  The K order inside an MMA is free as long as both operands agree:
-// word j of those 16 bytes holds columns 32 (lane % 4) + 8 j + 0..7, whose half
-// bytes i and i + 4 come out as one pair, and x is staged in shared memory in
-// that pair order, 16 bytes per (token, 8 columns).
+// side.  A warp streams the 1 KB of one group of its 16 rows at a time through a
+// cp.async ring of its own, so no barrier stands between the warps until their
+// sums meet.  The K order inside an MMA is free as long as both operands agree:
+// lane (g, t) = (lane / 4, lane % 4) takes word 4 j + t of rows g and g + 8, the
+// columns 8 (4 j + t) + 0..7, whose half bytes i and i + 4 come out as one pair,
+// and the same 8 columns of token g in the same pair order.  (The words lie in
+// shared memory with the 16-byte units of row r at j ^ (r / 2 % 4), which keeps a
+// warp's 32 words in 32 banks.)  8-bit x goes through f16, bf16 x through bf16.
 //
-// K is split over the CTAs of a cluster; each keeps its partial in shared
-// memory and the cluster adds them in rank order through distributed shared
-// memory, so a call needs no workspace and its result does not depend on timing.
+// K is split over the warps of a CTA and the CTAs of a cluster; each CTA keeps its
+// partials in shared memory and the cluster adds them in rank order through
+// distributed shared memory, so a call needs no workspace and its result does not
+// depend on timing.
 #include <cuda_fp16.h>
+#include <stdlib.h>
+
+#include <type_traits>
 
 #include "sm100.cuh"
 #include "w4.cuh"
@@ -34,8 +39,7 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 8;         // ring depth per thread, 32 bytes a stage
-constexpr int kChunkGroups = 8;    // groups of x staged at a time
+constexpr int kStages = 8;         // groups a warp has in flight or in use, 1 KB each
 constexpr int kMaxSplit = 8;       // CTAs of a cluster along K (the portable size)
 
 struct W4Params {
@@ -46,14 +50,22 @@ struct W4Params {
   uint16_t* y;          // [T, N] bf16
   int T, K, N, groups;
   int split, per;       // CTAs along K, groups per CTA
+  bool early;           // the weights may be read before the previous kernel has finished
 };
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+template <bool kF16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  if (kF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -61,171 +73,176 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-
-// Two E4M3 codes as a bf16 pair (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_bf16x2(f.x, f.y);
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
-// Eight bf16 values (four natural pairs) to the pair order (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ uint4 to_pair_order(uint4 v) {
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                    __byte_perm(v.y, v.w, 0x7632));
+// Two E4M3 codes (the low 16 bits) as an f16 pair, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  return h;
+}
+
+// Eight values of x, as loaded, to MMA operands in the pair order (0,4) (1,5) (2,6) (3,7).
+__device__ __forceinline__ void pair_order(const uint4& v, uint32_t (&b)[4]) {
+  b[0] = __byte_perm(v.x, v.z, 0x5410);
+  b[1] = __byte_perm(v.x, v.z, 0x7632);
+  b[2] = __byte_perm(v.y, v.w, 0x5410);
+  b[3] = __byte_perm(v.y, v.w, 0x7632);
+}
+__device__ __forceinline__ void pair_order(const uint2& v, uint32_t (&b)[4]) {
+  const uint32_t a = __byte_perm(v.x, v.y, 0x5140), c = __byte_perm(v.x, v.y, 0x7362);
+  b[0] = e4m3x2_to_f16x2(a);
+  b[1] = e4m3x2_to_f16x2(a >> 16);
+  b[2] = e4m3x2_to_f16x2(c);
+  b[3] = e4m3x2_to_f16x2(c >> 16);
 }
 
 // kRowWarps warps cover 16 rows each, the other kWarps / kRowWarps share their
 // groups of K; kTiles tiles of 8 tokens.
-template <int kRowWarps, int kTiles, bool kFp8>
+template <int kRowWarps, int kTiles>
 struct W4Shape {
   static constexpr int kKWarps = kWarps / kRowWarps;
   static constexpr int kRows = 16 * kRowWarps;
   static constexpr int kTok = 8 * kTiles;
   static constexpr int kLd = kRows + 4;  // floats per token of a partial: conflict-free fragment stores
-  static constexpr int kRing = kStages * kThreads * 32;
-  static constexpr int kX = kChunkGroups * kTok * kW4Group * 2;
-  static constexpr int kSx = kFp8 ? kChunkGroups * kTok * 4 : 0;
-  static constexpr int kSw = kChunkGroups * kRows * 4;
-  static constexpr int kPart = kKWarps * kTok * kLd * 4;
-  static constexpr int kSmem = kRing + kX + kSx + kSw + kPart;
+  static constexpr int kRing = kStages * kWarps * 1024;
+  static constexpr int kPart = kKWarps * kTok * kLd * 4;  // lies over the ring
+  static constexpr int kSmem = kRing > kPart ? kRing : kPart;
+};
+
+// What one group needs besides its weights.
+template <int kTiles, bool kFp8>
+struct W4Operands {
+  std::conditional_t<kFp8, uint2, uint4> x[kTiles][4];
+  float sx[kTiles][2];
+  float sw[2];
 };
 
 template <int kRowWarps, int kTiles, bool kFp8>
 __global__ void __launch_bounds__(kThreads)
 linear_w4_kernel(const W4Params p) {
-  using S = W4Shape<kRowWarps, kTiles, kFp8>;
+  using S = W4Shape<kRowWarps, kTiles>;
+  using Vec = std::conditional_t<kFp8, uint2, uint4>;  // 8 values of x
   extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* xs = smem + S::kRing;
-  float* sxs = reinterpret_cast<float*>(xs + S::kX);
-  float* sws = reinterpret_cast<float*>(xs + S::kX + S::kSx);
-  float* part = reinterpret_cast<float*>(xs + S::kX + S::kSx + S::kSw);
+  float* part = reinterpret_cast<float*>(smem);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lg = lane >> 2, lt = lane & 3;
   const int rw = warp % kRowWarps, kw = warp / kRowWarps;
   const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
   const int n0 = tile * S::kRows;
   const int t0 = blockIdx.z * S::kTok;
-  const int g0 = rank * p.per, g1 = min(p.groups, g0 + p.per);
-  grid_dep_wait();
-  grid_dep_launch();
+  const int g0 = rank * p.per + kw, g1 = min(p.groups, rank * p.per + p.per);
+  if (!p.early) grid_dep_wait();
 
-  // this thread's two rows and its 16 bytes (32 columns) of each group
-  const int r0 = n0 + rw * 16 + (lane >> 2);
+  const int r0 = n0 + rw * 16 + lg;
   const int64_t row_bytes = p.K >> 1;
-  const uint8_t* src0 = p.w4 + static_cast<int64_t>(r0) * row_bytes + (lane & 3) * 16;
-  const uint8_t* src1 = src0 + 8 * row_bytes;
+  const uint8_t* src0 = p.w4 + static_cast<int64_t>(r0) * row_bytes + lt * 16;
   const bool in0 = r0 < p.N, in1 = r0 + 8 < p.N;
-  const uint32_t ring = smem_u32(smem) + tid * 16;
-  // K is a multiple of 64: in the last group the upper two lanes may lie past the row
+  const uint32_t ring = smem_u32(smem) + warp * 1024;
+  const uint32_t sw_off = (lg >> 1 & 3) << 4;  // the row's 16-byte unit permutation
+  const uint32_t put = ring + lg * 64 + ((lt << 4) ^ sw_off);
+  const uint32_t get = ring + lg * 64 + lt * 4;
   auto fetch = [&](int g, int stage) {
-    const bool inside = g < g1 && static_cast<int64_t>(g) * 64 + (lane & 3) * 16 < row_bytes;
-    const uint32_t dst = ring + stage * (kThreads * 32);
+    // K is a multiple of 64: the last group may have only two of its four 16-byte units
     const int64_t at = static_cast<int64_t>(g) * 64;
+    const bool inside = g < g1 && at + lt * 16 < row_bytes;
     const bool a = inside && in0, b = inside && in1;
+    const uint32_t dst = put + stage * (kWarps * 1024);
     cp_async16_zfill(dst, a ? src0 + at : p.w4, a ? 16u : 0u);
-    cp_async16_zfill(dst + kThreads * 16, b ? src1 + at : p.w4, b ? 16u : 0u);
+    cp_async16_zfill(dst + 512, b ? src0 + 8 * row_bytes + at : p.w4, b ? 16u : 0u);
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(g0 + kw + s * S::kKWarps, s);
+  for (int s = 0; s < kStages - 1; ++s) fetch(g0 + s * S::kKWarps, s);
+  if (p.early) grid_dep_wait();
+  grid_dep_launch();
+
+  auto load = [&](int g, W4Operands<kTiles, kFp8>& o) {
+    if (g >= g1) return;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const int t = t0 + 8 * i + lg;
+      const Vec* row = reinterpret_cast<const Vec*>(static_cast<const uint8_t*>(p.x) +
+                                                    (static_cast<int64_t>(t) * p.K + g * kW4Group) * (kFp8 ? 1 : 2));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o.x[i][j] = t < p.T && g * kW4Group + 8 * (4 * j + lt) < p.K ? row[4 * j + lt] : Vec{};
+      if (kFp8) {
+        const int c = t0 + 8 * i + 2 * lt;
+        o.sx[i][0] = c < p.T ? p.sx[static_cast<int64_t>(c) * p.groups + g] : 0.f;
+        o.sx[i][1] = c + 1 < p.T ? p.sx[static_cast<int64_t>(c + 1) * p.groups + g] : 0.f;
+      }
+    }
+    o.sw[0] = in0 ? bf16_bits_to_f32(p.sw[static_cast<int64_t>(r0) * p.groups + g]) : 0.f;
+    o.sw[1] = in1 ? bf16_bits_to_f32(p.sw[static_cast<int64_t>(r0 + 8) * p.groups + g]) : 0.f;
+  };
 
   float acc[kTiles][4];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  W4Operands<kTiles, kFp8> next;
+  load(g0, next);
+  int stage = 0;
+  for (int g = g0; g < g1; g += S::kKWarps) {
+    const W4Operands<kTiles, kFp8> o = next;
+    load(g + S::kKWarps, next);
+    cp_async_wait_group<kStages - 2>();
+    __syncwarp();  // the group has landed for every lane, and every lane has read the one before
+    fetch(g + (kStages - 1) * S::kKWarps, stage == 0 ? kStages - 1 : stage - 1);
+    const uint32_t at = get + stage * (kWarps * 1024);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
 
-  int step = 0;  // this warp's groups so far
-  for (int gc = g0; gc < g1; gc += kChunkGroups) {
-    const int ng = min(kChunkGroups, g1 - gc);
-    __syncthreads();  // the previous chunk has been read
-    // x of these groups: one 16-byte unit per (token, 8 columns), zeros past T and K
-    for (int u = tid; u < S::kTok * ng * 16; u += kThreads) {
-      const int c = u % (ng * 16), t = u / (ng * 16);  // chunk of 8 columns, token
-      const int col = gc * kW4Group + c * 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (t0 + t < p.T && col < p.K) {
-        const int64_t at = static_cast<int64_t>(t0 + t) * p.K + col;
-        if (kFp8) {
-          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + at);
-          v = make_uint4(e4m3x2_to_bf16x2(q.x), e4m3x2_to_bf16x2(q.x >> 16), e4m3x2_to_bf16x2(q.y),
-                         e4m3x2_to_bf16x2(q.y >> 16));
-        } else {
-          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + at);
-        }
-      }
-      const int slot = (((c >> 4) * kTiles + (t >> 3)) * 4 + (c & 3)) * 32 + (t & 7) * 4 + ((c & 15) >> 2);
-      *reinterpret_cast<uint4*>(xs + slot * 16) = to_pair_order(v);
-    }
-    if (kFp8)
-      for (int u = tid; u < S::kTok * ng; u += kThreads) {
-        const int g = u % ng, t = u / ng;
-        sxs[g * S::kTok + t] = t0 + t < p.T ? p.sx[static_cast<int64_t>(t0 + t) * p.groups + gc + g] : 0.f;
-      }
-    for (int u = tid; u < S::kRows * ng; u += kThreads) {
-      const int g = u % ng, r = u / ng;
-      sws[g * S::kRows + r] =
-          n0 + r < p.N ? bf16_bits_to_f32(p.sw[static_cast<int64_t>(n0 + r) * p.groups + gc + g]) : 0.f;
-    }
-    __syncthreads();
-
-    for (int g = g0 + kw + step * S::kKWarps; g < gc + ng; g += S::kKWarps, ++step) {
-      fetch(g + (kStages - 1) * S::kKWarps, (step + kStages - 1) % kStages);
-      cp_async_wait_group<kStages - 1>();
-      const uint8_t* st = smem + (step % kStages) * (kThreads * 32) + tid * 16;
-      const uint4 wa = *reinterpret_cast<const uint4*>(st);
-      const uint4 wb = *reinterpret_cast<const uint4*>(st + kThreads * 16);
-      const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
-      float part_g[kTiles][4];
+    float sum[kTiles][4];
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) part_g[i][0] = part_g[i][1] = part_g[i][2] = part_g[i][3] = 0.f;
-      const int gl = g - gc;
+    for (int i = 0; i < kTiles; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t pa[4], pb[4];
-        w4_pairs(a[j], pa);
-        w4_pairs(b[j], pb);
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl * kTiles + i) * 4 + j) * 32 + lane) * 16);
-          mma_bf16(part_g[i], pa[0], pb[0], pa[1], pb[1], xv.x, xv.y);
-          mma_bf16(part_g[i], pa[2], pb[2], pa[3], pb[3], xv.z, xv.w);
-        }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t unit = (j << 4) ^ sw_off;
+      const uint32_t va = ld_shared_u32(at + unit), vb = ld_shared_u32(at + 512 + unit);
+      uint32_t a[4], b[4];
+      if (kFp8) {
+        w4_pairs_f16(va, a);
+        w4_pairs_f16(vb, b);
+      } else {
+        w4_pairs(va, a);
+        w4_pairs(vb, b);
       }
-      const float s0 = sws[gl * S::kRows + rw * 16 + (lane >> 2)];
-      const float s1 = sws[gl * S::kRows + rw * 16 + (lane >> 2) + 8];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
-        if (kFp8) {
-          const float2 q = *reinterpret_cast<const float2*>(sxs + gl * S::kTok + i * 8 + (lane & 3) * 2);
-          acc[i][0] = fmaf(part_g[i][0] * q.x, s0, acc[i][0]);
-          acc[i][1] = fmaf(part_g[i][1] * q.y, s0, acc[i][1]);
-          acc[i][2] = fmaf(part_g[i][2] * q.x, s1, acc[i][2]);
-          acc[i][3] = fmaf(part_g[i][3] * q.y, s1, acc[i][3]);
-        } else {
-          acc[i][0] = fmaf(part_g[i][0], s0, acc[i][0]);
-          acc[i][1] = fmaf(part_g[i][1], s0, acc[i][1]);
-          acc[i][2] = fmaf(part_g[i][2], s1, acc[i][2]);
-          acc[i][3] = fmaf(part_g[i][3], s1, acc[i][3]);
-        }
+        uint32_t x[4];
+        pair_order(o.x[i][j], x);
+        mma_16816<kFp8>(sum[i], a[0], b[0], a[1], b[1], x[0], x[1]);
+        mma_16816<kFp8>(sum[i], a[2], b[2], a[3], b[3], x[2], x[3]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = kFp8 ? sum[i][e] * o.sx[i][e & 1] : sum[i][e];
+        acc[i][e] = fmaf(v, o.sw[e >> 1], acc[i][e]);
+      }
   }
   cp_async_wait_all();
+  __syncthreads();  // the ring is done with: the partials take its place
 
   // partial [K warp][token][row]
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int t = i * 8 + (lane & 3) * 2 + (e & 1), r = rw * 16 + (lane >> 2) + (e >> 1) * 8;
+      const int t = i * 8 + lt * 2 + (e & 1), r = rw * 16 + lg + (e >> 1) * 8;
       part[(kw * S::kTok + t) * S::kLd + r] = acc[i][e];
     }
   if (p.split > 1) cluster_sync();
   else __syncthreads();
 
-  // rank q of the cluster adds and stores every split-th block of 16 rows' share:
-  // element e of (token, row) with row fastest, in rank order
+  // the cluster's threads share the (token, row) sums, row fastest, each in rank and warp order
   const int toks = min(S::kTok, p.T - t0);
   const uint32_t base = smem_u32(part);
   for (int e = rank * kThreads + tid; e < toks * S::kRows; e += p.split * kThreads) {
@@ -244,7 +261,7 @@ linear_w4_kernel(const W4Params p) {
 
 template <int kRowWarps, int kTiles, bool kFp8>
 cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
-  using S = W4Shape<kRowWarps, kTiles, kFp8>;
+  using S = W4Shape<kRowWarps, kTiles>;
   static bool configured[kMaxDevicesLocal] = {};  // the attribute is per device
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -257,6 +274,8 @@ cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
   const int tiles = (p.N + S::kRows - 1) / S::kRows;
   p.split = 1;
   while (p.split < kMaxSplit && tiles * p.split < 304 && p.groups >= 2 * p.split * S::kKWarps) p.split *= 2;
+  if (getenv("W4_SPLIT")) p.split = atoi(getenv("W4_SPLIT"));
+  p.early = launch_overlap() >= 2;
   p.per = (p.groups + p.split - 1) / p.split;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -274,18 +293,27 @@ cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <bool kFp8, int kTiles>
+cudaError_t launch_rw(const W4Params& p, cudaStream_t stream) {
+  const int rw = getenv("W4_RW") ? atoi(getenv("W4_RW")) : 4;
+  if (rw == 1) return launch_shape<1, kTiles, kFp8>(p, stream);
+  if (rw == 2) return launch_shape<2, kTiles, kFp8>(p, stream);
+  if (rw == 4) return launch_shape<4, kTiles, kFp8>(p, stream);
+  return launch_shape<8, kTiles, kFp8>(p, stream);
+}
+
 template <bool kFp8>
 cudaError_t launch_any(const W4Params& p, cudaStream_t stream) {
-  if (p.T <= 8) return launch_shape<4, 1, kFp8>(p, stream);
-  if (p.T <= 16) return launch_shape<4, 2, kFp8>(p, stream);
-  return launch_shape<4, 4, kFp8>(p, stream);
+  if (p.T <= 8) return launch_rw<kFp8, 1>(p, stream);
+  if (p.T <= 16) return launch_rw<kFp8, 2>(p, stream);
+  return launch_rw<kFp8, 4>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_w4(const void* x, const float* x_scale, const uint8_t* w4, const uint16_t* w_scale,
                              uint16_t* y, int T, int K, int N, cudaStream_t stream) {
-  W4Params p{x, x_scale, w4, w_scale, y, T, K, N, w4_groups(K), 1, 0};
+  W4Params p{x, x_scale, w4, w_scale, y, T, K, N, w4_groups(K), 1, 0, false};
   return x_scale != nullptr ? launch_any<true>(p, stream) : launch_any<false>(p, stream);
 }
 

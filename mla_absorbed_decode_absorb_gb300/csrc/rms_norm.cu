@@ -10,13 +10,14 @@
 // formula needs (the sum of squares, then the scaling), so x and r are read
 // once.  The sum, h and y stay in fp32: y comes from the unrounded h, and each
 // output is rounded once.  A group of 128 columns is 16 neighbouring lanes of 8
-// columns each, so its maximum is four shuffles.
+// columns each, so its maximum is four shuffles, and its codes are v * (1 / s),
+// one IEEE division per group.  Bound by HBM for many rows, by the launch and one
+// round trip to memory for few (1 x 7168: 1.9 us).
 #include "append_row.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kMaxThreads = 1024;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
 struct NormParams {
@@ -28,7 +29,7 @@ struct NormParams {
   uint8_t* y8;            // 8-bit output, or nullptr
   float* s8;
   int64_t x_ld;
-  int D, groups;
+  int T, D, groups;
   float eps;
 };
 
@@ -51,43 +52,47 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// kChunks chunks of 8 columns per thread: chunk i of a thread is threadIdx.x +
-// i * blockDim.x, and blockDim.x is a multiple of 32, so 16 neighbouring lanes
-// always hold one whole group of 128 columns.
-template <int kChunks>
-__global__ void __launch_bounds__(kMaxThreads)
+// kChunks chunks of 8 columns per thread: chunk i of a thread is its index in
+// the row + i * kSpan, kSpan threads to a row.  kSpan is a multiple of 32, so 16
+// neighbouring lanes always hold one whole group of 128 columns.  kSpan = 32: a
+// warp per row, kThreads / 32 rows per CTA; otherwise one row per CTA, which may
+// have fewer threads than kThreads (kSpan = 0).
+template <int kChunks, int kThreads, int kSpan>
+__global__ void __launch_bounds__(kThreads)
 rms_norm_kernel(const NormParams p) {
-  __shared__ float warp_sum[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x;
+  __shared__ float warp_sum[kSpan == 32 ? 1 : 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = kSpan == 32 ? lane : static_cast<int>(threadIdx.x);
+  const int span = kSpan == 32 ? 32 : static_cast<int>(blockDim.x);
+  const int64_t row = kSpan == 32 ? static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp : blockIdx.x;
   const int chunks = p.D >> 3;
   grid_dep_wait();
   grid_dep_launch();
+  if (kSpan == 32 && row >= p.T) return;
 
   const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.x_ld);
   const int64_t base = row * chunks;
-  uint4 xv[kChunks], rv[kChunks], wv[kChunks];
+  uint4 xv[kChunks], rv[kChunks];
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int c = tid + i * static_cast<int>(blockDim.x);
-    xv[i] = rv[i] = wv[i] = make_uint4(0, 0, 0, 0);
+    const int c = tid + i * span;
+    xv[i] = rv[i] = make_uint4(0, 0, 0, 0);
     if (c < chunks) {
       xv[i] = x[c];
       if (p.r != nullptr) rv[i] = reinterpret_cast<const uint4*>(p.r)[base + c];
-      wv[i] = reinterpret_cast<const uint4*>(p.w)[c];
     }
   }
   float h[kChunks][8];
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
+    const int c = tid + i * span;
     unpack8(xv[i], h[i]);
     if (p.r != nullptr) {
       float r[8];
       unpack8(rv[i], r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[i][e] += r[e];
-      const int c = tid + i * static_cast<int>(blockDim.x);
       if (c < chunks) reinterpret_cast<uint4*>(p.r_out)[base + c] = pack8(h[i]);
     }
 #pragma unroll
@@ -95,20 +100,21 @@ rms_norm_kernel(const NormParams p) {
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) warp_sum[warp] = sum;
-  __syncthreads();
-  // every warp adds the warps' sums in the same order
-  const int warps = blockDim.x >> 5;
-  sum = lane < warps ? warp_sum[lane] : 0.f;
+  if (kSpan != 32) {
+    if (lane == 0) warp_sum[warp] = sum;
+    __syncthreads();
+    // every warp adds the warps' sums in the same order
+    sum = lane < static_cast<int>(blockDim.x >> 5) ? warp_sum[lane] : 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
   const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(p.D)) + p.eps));
 
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int c = tid + i * static_cast<int>(blockDim.x);
+    const int c = tid + i * span;
     float w[8];
-    unpack8(wv[i], w);
+    unpack8(c < chunks ? reinterpret_cast<const uint4*>(p.w)[c] : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * inv * w[e];
     if (p.y != nullptr && c < chunks) reinterpret_cast<uint4*>(p.y)[base + c] = pack8(h[i]);
@@ -119,9 +125,10 @@ rms_norm_kernel(const NormParams p) {
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
       const float s = fmaxf(__fdiv_rn(a, 448.f), kScaleFloor);
+      const float rs = __fdiv_rn(1.f, s);
       uint16_t q[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = e4m3x2(__fdiv_rn(h[i][2 * e], s), __fdiv_rn(h[i][2 * e + 1], s));
+      for (int e = 0; e < 4; ++e) q[e] = e4m3x2(h[i][2 * e] * rs, h[i][2 * e + 1] * rs);
       if (c < chunks) {
         reinterpret_cast<uint2*>(p.y8)[base + c] =
             make_uint2(q[0] | (static_cast<uint32_t>(q[1]) << 16), q[2] | (static_cast<uint32_t>(q[3]) << 16));
@@ -131,16 +138,31 @@ rms_norm_kernel(const NormParams p) {
   }
 }
 
+template <int kChunks, int kThreads, int kSpan>
+cudaError_t launch_shape(const NormParams& p, cudaStream_t stream) {
+  const int chunks = p.D >> 3;
+  const int rows = kSpan == 32 ? kThreads / 32 : 1;
+  const int threads = kSpan == 32 ? kThreads : ((chunks + kChunks - 1) / kChunks + 31) / 32 * 32;
+  return launch_kernel(rms_norm_kernel<kChunks, kThreads, kSpan>, dim3((p.T + rows - 1) / rows), dim3(threads), 0,
+                       stream, p);
+}
+
 }  // namespace
 
 cudaError_t launch_rms_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual, uint16_t* residual_out,
                             const uint16_t* w, float eps, uint16_t* y, uint8_t* y8, float* y8_scale, int T, int D,
                             cudaStream_t stream) {
-  const NormParams p{x, residual, w, residual_out, y, y8, y8_scale, x_ld, D, (D + 127) / 128, eps};
+  const NormParams p{x, residual, w, residual_out, y, y8, y8_scale, x_ld, T, D, (D + 127) / 128, eps};
   const int chunks = D >> 3;
-  auto threads = [&](int per) { return dim3(((chunks + per - 1) / per + 31) / 32 * 32); };
-  if (chunks <= kMaxThreads) return launch_kernel(rms_norm_kernel<1>, dim3(T), threads(1), 0, stream, p);
-  return launch_kernel(rms_norm_kernel<2>, dim3(T), threads(2), 0, stream, p);
+  // 512 columns or fewer in many rows: a warp per row (16384 x 512: 8.1 us, against 17.5 with a CTA of two warps
+  // per row, which the rate of CTA launches bounds; 256 rows: 1.8 against 1.6 us)
+  if (chunks <= 64 && T >= 1024) return launch_shape<2, 256, 32>(p, stream);
+  // one chunk per thread while the rows fit the GPU at once (32 x 1536: 1.8 us, against 2.1 with two chunks;
+  // 128 x 7168: 3.4 against 3.9), then two, which keep twice the bytes in flight per register (16384 x 7168 with
+  // the residual, 8-bit output: 120 us against 155, 1.02 of the measured copy bandwidth; four chunks: 122)
+  if (chunks <= 1024 && static_cast<int64_t>(T) * chunks <= 152 * 2048) return launch_shape<1, 1024, 0>(p, stream);
+  if (chunks <= 1024) return launch_shape<2, 512, 0>(p, stream);
+  return launch_shape<4, 512, 0>(p, stream);  // up to 16384 columns (8192 rows: 156 us, 1.01)
 }
 
 }  // namespace mla

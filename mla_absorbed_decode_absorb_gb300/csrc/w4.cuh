@@ -23,4 +23,17 @@ __device__ __forceinline__ void w4_pairs(uint32_t v, uint32_t (&p)[4]) {
   }
 }
 
+
+// The same pairs in f16: 0x6400 is 1024, whose unit in the last place is 1, so a half byte
+// in the low bits adds u and one four bits up adds 16 u; both ways back are exact.
+__device__ __forceinline__ void w4_pairs_f16(uint32_t v, uint32_t (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = ((v >> (8 * i)) & 0x000f000fu) | 0x64006400u;  // 1024 + u
+    const uint32_t hi = ((v >> (8 * i)) & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 u
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p[2 * i]) : "r"(lo), "r"(0x64086408u));                       // - 1032
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[2 * i + 1]) : "r"(hi), "r"(0x2c002c00u), "r"(0xd480d480u));  // / 16 - 72
+  }
+}
+
 }  // namespace mla

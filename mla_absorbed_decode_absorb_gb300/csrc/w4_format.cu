@@ -3,37 +3,59 @@
 //   s = bf16(max|w| / 7) over each 128 columns of a row (1 where that is zero)
 //   u = clamp(round(w / s), -8, 7) + 8        w' = bf16((u - 8) s)
 //
-// Every step is one IEEE operation on exactly representable values (a quotient
-// of two bf16 values is never so near a tie that fp32 rounds it across), so the
-// codes are reproducible bit for bit.  16 lanes hold a group, 8 columns each;
-// both kernels stream and are bound by HBM.
+// The codes are those of exact arithmetic.  w and s have 8 significant bits, so
+// a quotient w / s of at most 8 is either a tie k + 1/2 exactly or at least
+// 2^-10 away from one.  w * (1 / s) is off by at most 2^-20 there; added to
+// 3 * 2^10, whose unit in the last place is 2^-12, it is rounded to a multiple of
+// 2^-12: a tie becomes the tie again and nothing else becomes one.  (Eight IEEE
+// divisions a thread cost more than the traffic.)  The scale max / 7 is rounded
+// from its fp32 quotient, which is never near a tie of bf16 neighbours.
+//
+// 16 lanes hold a group, 8 columns each; a thread has kUnits groups in flight,
+// kThreads / 16 apart.  Both kernels stream.
 #include "w4.cuh"
 
 namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnits = 4;                           // groups per thread
+constexpr int kPerBlock = kThreads / 16 * kUnits;   // groups per CTA
 
+// Where unit u (a group of 128 columns of one row) and lane `sub` of it lie:
+// element offset of its 8 columns, and whether they exist.  K % 128 = 0 makes the
+// weight one run of groups; else (kRagged) a row's last group has 64 columns.
+template <bool kRagged>
+__device__ __forceinline__ bool w4_place(uint32_t u, uint32_t units, uint32_t groups, int K, int sub, int64_t* at) {
+  if (!kRagged) {
+    *at = static_cast<int64_t>(u) * kW4Group + sub * 8;
+    return u < units;
+  }
+  const uint32_t row = u / groups;
+  const int col = static_cast<int>(u - row * groups) * kW4Group + sub * 8;
+  *at = static_cast<int64_t>(row) * K + col;
+  return u < units && col < K;
+}
+
+template <bool kRagged>
 __global__ void __launch_bounds__(kThreads)
 quantize_w4_kernel(const uint16_t* __restrict__ w, uint32_t* __restrict__ w4, uint16_t* __restrict__ scale,
                    uint32_t units, uint32_t groups, int K) {
   grid_dep_wait();
   grid_dep_launch();
-  // unit = one group of one row; the 16 lanes of a half warp share it
   const int sub = threadIdx.x & 15;
-  const uint32_t per_block = kThreads / 16;
-  for (uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * per_block; u0 < units;
-       u0 += static_cast<uint64_t>(gridDim.x) * per_block) {
-    const uint64_t u = u0 + (threadIdx.x >> 4);
-    const bool here = u < units;
-    const uint32_t row = here ? static_cast<uint32_t>(u) / groups : 0;
-    const uint32_t g = here ? static_cast<uint32_t>(u) - row * groups : 0;
-    const int col = static_cast<int>(g) * kW4Group + sub * 8;
-    const bool in = here && col < K;
-    const int64_t at = static_cast<int64_t>(row) * K + col;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (in) v = *reinterpret_cast<const uint4*>(w + at);
-    const uint32_t bits[4] = {v.x, v.y, v.z, v.w};
+  const uint32_t u0 = blockIdx.x * kPerBlock + (threadIdx.x >> 4);
+  uint4 v[kUnits];
+  int64_t at[kUnits];
+  bool in[kUnits];
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    in[q] = w4_place<kRagged>(u0 + q * (kThreads / 16), units, groups, K, sub, &at[q]);
+    v[q] = in[q] ? *reinterpret_cast<const uint4*>(w + at[q]) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    const uint32_t bits[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -47,61 +69,70 @@ quantize_w4_kernel(const uint16_t* __restrict__ w, uint32_t* __restrict__ w4, ui
     for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     uint16_t sb = f32_to_bf16_bits(__fdiv_rn(a, 7.f));
     if (sb == 0) sb = 0x3f80;  // a group of zeros (or below bf16's smallest scale): s = 1
-    const float s = bf16_bits_to_f32(sb);
+    float s = bf16_bits_to_f32(sb);
+    const float lift = s < 0x1p-100f ? 0x1p64f : 1.f;  // the reciprocal of a tiny scale would overflow
+    const float rs = __fdiv_rn(1.f, s * lift);
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -8.f), 7.f);
-      word |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * i);
+      const float c = rintf(__fsub_rn(fmaf(x[i] * lift, rs, 3072.f), 3072.f));
+      // c + 8 + 2^23 holds the code in its low bits
+      word |= (__float_as_uint(fminf(fmaxf(c, -8.f), 7.f) + 8388616.f) & 15u) << (4 * i);
     }
-    if (in) w4[at >> 3] = word;
-    if (here && sub == 0) scale[u] = sb;
+    const uint32_t u = u0 + q * (kThreads / 16);
+    if (in[q]) w4[at[q] >> 3] = word;
+    if (u < units && sub == 0) scale[u] = sb;
   }
 }
 
+template <bool kRagged>
 __global__ void __launch_bounds__(kThreads)
 dequantize_w4_kernel(const uint32_t* __restrict__ w4, const uint16_t* __restrict__ scale, uint16_t* __restrict__ w,
                      uint32_t units, uint32_t groups, int K) {
   grid_dep_wait();
   grid_dep_launch();
   const int sub = threadIdx.x & 15;
-  const uint32_t per_block = kThreads / 16;
-  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * per_block + (threadIdx.x >> 4); u < units;
-       u += static_cast<uint64_t>(gridDim.x) * per_block) {
-    const uint32_t row = static_cast<uint32_t>(u) / groups;
-    const int col = static_cast<int>(static_cast<uint32_t>(u) - row * groups) * kW4Group + sub * 8;
-    if (col >= K) continue;
-    const int64_t at = static_cast<int64_t>(row) * K + col;
-    const uint32_t v = w4[at >> 3];
-    const float s = bf16_bits_to_f32(scale[u]);
-    uint32_t out[4];
+  const uint32_t u0 = blockIdx.x * kPerBlock + (threadIdx.x >> 4);
+  uint32_t v[kUnits], s[kUnits];
+  int64_t at[kUnits];
+  bool in[kUnits];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int lo = static_cast<int>((v >> (8 * i)) & 15u) - 8, hi = static_cast<int>((v >> (8 * i + 4)) & 15u) - 8;
-      const __nv_bfloat162 b = __floats2bfloat162_rn(static_cast<float>(lo) * s, static_cast<float>(hi) * s);
-      out[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *reinterpret_cast<uint4*>(w + at) = make_uint4(out[0], out[1], out[2], out[3]);
+  for (int q = 0; q < kUnits; ++q) {
+    const uint32_t u = u0 + q * (kThreads / 16);
+    in[q] = w4_place<kRagged>(u, units, groups, K, sub, &at[q]);
+    v[q] = in[q] ? w4[at[q] >> 3] : 0;
+    s[q] = in[q] ? scale[u] * 0x10001u : 0;  // the scale in both halves
+  }
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    uint32_t p[4];
+    w4_pairs(v[q], p);
+    // (u - 8) s has 12 significant bits: the bf16 product is the rounded exact one
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(p[i]), "r"(s[q]));
+    if (in[q])
+      *reinterpret_cast<uint4*>(w + at[q]) =
+          make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                     __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
   }
 }
 
-unsigned blocks_for(uint32_t units) {
-  const uint64_t want = (static_cast<uint64_t>(units) + kThreads / 16 - 1) / (kThreads / 16);
-  return static_cast<unsigned>(want < (1u << 30) ? want : (1u << 30));
-}
+unsigned blocks_for(uint32_t units) { return static_cast<unsigned>((static_cast<uint64_t>(units) + kPerBlock - 1) / kPerBlock); }
 
 }  // namespace
 
 cudaError_t launch_quantize_w4(const uint16_t* w, uint8_t* w4, uint16_t* scale, int N, int K, cudaStream_t stream) {
   const uint32_t groups = w4_groups(K), units = static_cast<uint32_t>(N) * groups;
-  return launch_kernel(quantize_w4_kernel, dim3(blocks_for(units)), dim3(kThreads), 0, stream, w,
+  auto kernel = K % kW4Group != 0 ? quantize_w4_kernel<true> : quantize_w4_kernel<false>;
+  return launch_kernel(kernel, dim3(blocks_for(units)), dim3(kThreads), 0, stream, w,
                        reinterpret_cast<uint32_t*>(w4), scale, units, groups, K);
 }
 
 cudaError_t launch_dequantize_w4(const uint8_t* w4, const uint16_t* scale, uint16_t* w, int N, int K,
                                  cudaStream_t stream) {
   const uint32_t groups = w4_groups(K), units = static_cast<uint32_t>(N) * groups;
-  return launch_kernel(dequantize_w4_kernel, dim3(blocks_for(units)), dim3(kThreads), 0, stream,
+  auto kernel = K % kW4Group != 0 ? dequantize_w4_kernel<true> : dequantize_w4_kernel<false>;
+  return launch_kernel(kernel, dim3(blocks_for(units)), dim3(kThreads), 0, stream,
                        reinterpret_cast<const uint32_t*>(w4), scale, w, units, groups, K);
 }
 

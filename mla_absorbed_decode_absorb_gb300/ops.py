@@ -97,9 +97,17 @@ def _check(where: str, status: int) -> None:
         raise MLAError(where, status)
 
 
+def _device() -> int:
+    """The current device, on which the kernels run."""
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getDevice()
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle of torch.cuda.current_stream(), without building its Python object
+        return torch._C._cuda_getCurrentRawStream(_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -248,40 +256,50 @@ def _groups(n: int) -> int:
     return (n + W4_GROUP - 1) // W4_GROUP
 
 
-def _on_current_device(first: torch.Tensor, *others):
-    """The kernels run on the current device: tensors of another one are refused."""
-    for t in (first, *others):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("expected a torch.Tensor")
-        if t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _arg(t, name: str, dtype, shape, device: int) -> int:
+    """As :func:`_dev`, for a tensor of the current device (one of another device is refused): single-token
+    calls take less time on the GPU than their checks on the host, so the usual case is one expression."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _matrix(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.shape
+
+
+def _new(shape, dtype, like):
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream):
-    if x.dim() != 2:
-        raise ValueError("x must be [T, D]")
-    T, D = x.shape
-    if not x.is_cuda or x.dtype != torch.bfloat16:
-        raise TypeError("x must be a CUDA bf16 tensor")
+    T, D = shape = x.shape
+    dev = _device()
+    if x.get_device() != dev:
+        raise ValueError(f"x is on {x.device}, the current device is cuda:{dev}")
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be torch.bfloat16, got {x.dtype}")
     if D > 1 and x.stride(1) != 1:
         raise ValueError("x's columns must be contiguous")
-    x_ld = x.stride(0) if T > 1 else max(D, 8)
-    if residual is not None and residual_out is None:
-        residual_out = residual
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out without residual")
-    _on_current_device(x, weight, residual, residual_out, y, y8, y_scale)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without residual")
+        r = r_out = None
+    else:
+        r = _arg(residual, "residual", torch.bfloat16, shape, dev)
+        r_out = r if residual_out is None else _arg(residual_out, "residual_out", torch.bfloat16, shape, dev)
     _check("mla_rms_norm", lib.mla_rms_norm(
-        x.data_ptr(), int(x_ld),
-        0 if residual is None else _dev(residual, "residual", torch.bfloat16, (T, D)),
-        0 if residual is None else _dev(residual_out, "residual_out", torch.bfloat16, (T, D)),
-        _dev(weight, "weight", torch.bfloat16, (D,)), float(eps),
-        0 if y is None else _dev(y, "y", torch.bfloat16, (T, D)),
-        0 if y8 is None else _dev(y8, "y8", torch.uint8, (T, D)),
-        0 if y_scale is None else _dev(y_scale, "y_scale", torch.float32, (T, _groups(D))),
-        int(T), int(D), _stream(stream)))
+        x.data_ptr(), x.stride(0) if T > 1 else D, r, r_out, _arg(weight, "weight", torch.bfloat16, (D,), dev), eps,
+        None if y is None else _arg(y, "y", torch.bfloat16, shape, dev),
+        None if y8 is None else _arg(y8, "y8", torch.uint8, shape, dev),
+        None if y_scale is None else _arg(y_scale, "y_scale", torch.float32, (T, _groups(D)), dev),
+        T, D, _stream(stream)))
 
 
 def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, stream=None):
@@ -289,8 +307,9 @@ def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, 
 
     x [T, D] may have a row stride (a multiple of 8); with ``residual`` the sum h is written to
     ``residual_out`` (default: in place)."""
+    shape = _matrix(x, "x")
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        y = _new(shape, torch.bfloat16, x)
     _rms_norm(x, weight, eps, residual, residual_out, y, None, None, stream)
     return y
 
@@ -299,65 +318,64 @@ def mla_rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y8=N
                      stream=None):
     """:func:`mla_rms_norm` with an 8-bit output: (E4M3 codes [T, D] uint8, scales [T, ceil(D/128)] float32),
     what ``mla_linear_w4_fp8`` reads.  With ``y`` the bf16 output is written too."""
+    T, D = shape = _matrix(x, "x")
     if y8 is None:
-        y8 = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        y8 = _new(shape, torch.uint8, x)
     if y_scale is None:
-        y_scale = torch.empty(x.shape[0], _groups(x.shape[-1]), dtype=torch.float32, device=x.device)
+        y_scale = _new((T, _groups(D)), torch.float32, x)
     _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream)
     return y8, y_scale
 
 
 def mla_quantize_w4(w, w4=None, w_scale=None, stream=None):
     """4-bit weights of ``w [N, K]`` bf16: (half bytes [N, K/2] uint8, scales [N, ceil(K/128)] bf16)."""
-    N, K = w.shape
+    N, K = shape = _matrix(w, "w")
+    dev, codes, scales = _device(), (N, K // 2), (N, _groups(K))
     if w4 is None:
-        w4 = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device)
+        w4 = _new(codes, torch.uint8, w)
     if w_scale is None:
-        w_scale = torch.empty(N, _groups(K), dtype=torch.bfloat16, device=w.device)
-    _on_current_device(w, w4, w_scale)
+        w_scale = _new(scales, torch.bfloat16, w)
     _check("mla_quantize_w4", lib.mla_quantize_w4(
-        _dev(w, "w", torch.bfloat16), _dev(w4, "w4", torch.uint8, (N, K // 2)),
-        _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))), int(N), int(K), _stream(stream)))
+        _arg(w, "w", torch.bfloat16, shape, dev), _arg(w4, "w4", torch.uint8, codes, dev),
+        _arg(w_scale, "w_scale", torch.bfloat16, scales, dev), N, K, _stream(stream)))
     return w4, w_scale
 
 
 def mla_dequantize_w4(w4, w_scale, w=None, stream=None):
     """``w [N, K]`` bf16 of 4-bit weights."""
-    N, K = w4.shape[0], 2 * w4.shape[1]
+    N, half = codes = _matrix(w4, "w4")
+    K, dev = 2 * half, _device()
     if w is None:
-        w = torch.empty(N, K, dtype=torch.bfloat16, device=w4.device)
-    _on_current_device(w4, w_scale, w)
+        w = _new((N, K), torch.bfloat16, w4)
     _check("mla_dequantize_w4", lib.mla_dequantize_w4(
-        _dev(w4, "w4", torch.uint8, (N, K // 2)), _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))),
-        _dev(w, "w", torch.bfloat16, (N, K)), int(N), int(K), _stream(stream)))
+        _arg(w4, "w4", torch.uint8, codes, dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev),
+        _arg(w, "w", torch.bfloat16, (N, K), dev), N, K, _stream(stream)))
     return w
 
 
 def mla_linear_w4(x, w4, w_scale, y=None, stream=None):
     """``y [T, N] = x [T, K] w^T`` in bf16 with 4-bit weights (fp32 accumulation, no workspace)."""
-    T, K = x.shape
-    N = w4.shape[0]
+    T, K = shape = _matrix(x, "x")
+    N, dev = _matrix(w4, "w4")[0], _device()
     if y is None:
-        y = torch.empty(T, N, dtype=torch.bfloat16, device=x.device)
-    _on_current_device(x, w4, w_scale, y)
+        y = _new((T, N), torch.bfloat16, x)
     _check("mla_linear_w4", lib.mla_linear_w4(
-        _dev(x, "x", torch.bfloat16, (T, K)), _dev(w4, "w4", torch.uint8, (N, K // 2)),
-        _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))), _dev(y, "y", torch.bfloat16, (T, N)),
-        int(T), int(K), int(N), _stream(stream)))
+        _arg(x, "x", torch.bfloat16, shape, dev), _arg(w4, "w4", torch.uint8, (N, K // 2), dev),
+        _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev), _arg(y, "y", torch.bfloat16, (T, N), dev),
+        T, K, N, _stream(stream)))
     return y
 
 
 def mla_linear_w4_fp8(x8, x_scale, w4, w_scale, y=None, stream=None):
     """:func:`mla_linear_w4` of 8-bit activations as :func:`mla_rms_norm_fp8` returns them."""
-    T, K = x8.shape
-    N = w4.shape[0]
+    T, K = shape = _matrix(x8, "x8")
+    N, dev, groups = _matrix(w4, "w4")[0], _device(), _groups(K)
     if y is None:
-        y = torch.empty(T, N, dtype=torch.bfloat16, device=x8.device)
-    _on_current_device(x8, x_scale, w4, w_scale, y)
+        y = _new((T, N), torch.bfloat16, x8)
     _check("mla_linear_w4_fp8", lib.mla_linear_w4_fp8(
-        _dev(x8, "x8", torch.uint8, (T, K)), _dev(x_scale, "x_scale", torch.float32, (T, _groups(K))),
-        _dev(w4, "w4", torch.uint8, (N, K // 2)), _dev(w_scale, "w_scale", torch.bfloat16, (N, _groups(K))),
-        _dev(y, "y", torch.bfloat16, (T, N)), int(T), int(K), int(N), _stream(stream)))
+        _arg(x8, "x8", torch.uint8, shape, dev), _arg(x_scale, "x_scale", torch.float32, (T, groups), dev),
+        _arg(w4, "w4", torch.uint8, (N, K // 2), dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, groups), dev),
+        _arg(y, "y", torch.bfloat16, (T, N), dev), T, K, N, _stream(stream)))
     return y
 
 
@@ -366,19 +384,19 @@ def mla_read_kv_fp8(cache_fp8, page_table, kv_lens, max_kv_len, rows=None, strea
     page table is ``arange(B * P).view(B, P)``.  Rows past a sequence's length are left as they were (rows
     allocated here are NaN there, as in an empty cache)."""
     c8, scale, kr = cache_fp8
-    B, P = int(kv_lens.shape[0]), int(c8.shape[0])
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages]")
-    shape = (B * ((int(max_kv_len) + 63) // 64), 64, D_ROW)
+    dev, max_kv_len = _device(), int(max_kv_len)
+    B, P = kv_lens.shape[0], c8.shape[0]
+    slots = _matrix(page_table, "page_table")[1]
+    shape = (B * ((max_kv_len + 63) // 64), 64, D_ROW)
     if rows is None:
         rows = empty_cache(shape[0], c8.device)
-    _on_current_device(c8, scale, kr, page_table, kv_lens, rows)
     _check("mla_read_kv_fp8", lib.mla_read_kv_fp8(
-        _dev(c8, "cache_c8", torch.uint8, (P, 64, D_LATENT)), _dev(scale, "cache_scale", torch.float32, (P, 64)),
-        _dev(kr, "cache_kr", torch.float16, (P, 64, D_ROPE)), P,
-        _dev(page_table, "page_table", torch.int32), int(page_table.shape[1]),
-        _dev(kv_lens, "kv_lens", torch.int32, (B,)), int(B), int(max_kv_len),
-        _dev(rows, "rows", torch.bfloat16, shape), _stream(stream)))
+        _arg(c8, "cache_c8", torch.uint8, (P, 64, D_LATENT), dev),
+        _arg(scale, "cache_scale", torch.float32, (P, 64), dev),
+        _arg(kr, "cache_kr", torch.float16, (P, 64, D_ROPE), dev), P,
+        _arg(page_table, "page_table", torch.int32, (B, slots), dev), slots,
+        _arg(kv_lens, "kv_lens", torch.int32, (B,), dev), B, max_kv_len,
+        _arg(rows, "rows", torch.bfloat16, shape, dev), _stream(stream)))
     return rows
 
 
