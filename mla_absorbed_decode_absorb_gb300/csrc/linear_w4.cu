@@ -39,7 +39,6 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 8;         // groups a warp has in flight or in use, 1 KB each
 constexpr int kMaxSplit = 8;       // CTAs of a cluster along K (the portable size)
 
 struct W4Params {
@@ -53,19 +52,27 @@ struct W4Params {
   bool early;           // the weights may be read before the previous kernel has finished
 };
 
-template <bool kF16>
+// c (+)= a b; with kFirst, c = a b.
+template <bool kF16, bool kFirst>
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  if (kF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+#define MLA_MMA_16816(type)                                                                                      \
+  if (kFirst)                                                                                                    \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "       \
+        "{%8, %9}, {%10, %10, %10, %10};"                                                                        \
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                                                         \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));                                       \
+  else                                                                                                           \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." type "." type ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "       \
+        "{%8, %9}, {%0, %1, %2, %3};"                                                                            \
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                         \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if (kF16) {
+    MLA_MMA_16816("f16");
+  } else {
+    MLA_MMA_16816("bf16");
+  }
+#undef MLA_MMA_16816
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -78,7 +85,6 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-
 // Two E4M3 codes (the low 16 bits) as an f16 pair, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   uint32_t h;
@@ -86,164 +92,180 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   return h;
 }
 
-// Eight values of x, as loaded, to MMA operands in the pair order (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ void pair_order(const uint4& v, uint32_t (&b)[4]) {
-  b[0] = __byte_perm(v.x, v.z, 0x5410);
-  b[1] = __byte_perm(v.x, v.z, 0x7632);
-  b[2] = __byte_perm(v.y, v.w, 0x5410);
-  b[3] = __byte_perm(v.y, v.w, 0x7632);
+// Eight values of x, as loaded, as MMA operands in the pair order (0,4) (1,5) (2,6) (3,7).
+__device__ __forceinline__ uint4 pair_order(const uint4& v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
 }
-__device__ __forceinline__ void pair_order(const uint2& v, uint32_t (&b)[4]) {
+__device__ __forceinline__ uint4 pair_order(const uint2& v) {
   const uint32_t a = __byte_perm(v.x, v.y, 0x5140), c = __byte_perm(v.x, v.y, 0x7362);
-  b[0] = e4m3x2_to_f16x2(a);
-  b[1] = e4m3x2_to_f16x2(a >> 16);
-  b[2] = e4m3x2_to_f16x2(c);
-  b[3] = e4m3x2_to_f16x2(c >> 16);
+  return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(c), e4m3x2_to_f16x2(c >> 16));
 }
 
-// kRowWarps warps cover 16 rows each, the other kWarps / kRowWarps share their
-// groups of K; kTiles tiles of 8 tokens.
-template <int kRowWarps, int kTiles>
+constexpr int kTok = 8;  // tokens of a CTA: the columns of one MMA
+
+// kRowWarps warps cover 16 kM rows each, the other kWarps / kRowWarps share their groups of K.
+template <int kRowWarps, int kM, int kStages>
 struct W4Shape {
   static constexpr int kKWarps = kWarps / kRowWarps;
-  static constexpr int kRows = 16 * kRowWarps;
-  static constexpr int kTok = 8 * kTiles;
-  static constexpr int kLd = kRows + 4;  // floats per token of a partial: conflict-free fragment stores
-  static constexpr int kRing = kStages * kWarps * 1024;
+  static constexpr int kRows = 16 * kM * kRowWarps;
+  static constexpr int kLd = kRows + 4;          // floats per token of a partial: conflict-free fragment stores
+  static constexpr int kStage = kWarps * kM * 1024;
   static constexpr int kPart = kKWarps * kTok * kLd * 4;  // lies over the ring
-  static constexpr int kSmem = kRing > kPart ? kRing : kPart;
+  static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
 };
 
-// What one group needs besides its weights.
-template <int kTiles, bool kFp8>
-struct W4Operands {
-  std::conditional_t<kFp8, uint2, uint4> x[kTiles][4];
-  float sx[kTiles][2];
-  float sw[2];
-};
-
-template <int kRowWarps, int kTiles, bool kFp8>
-__global__ void __launch_bounds__(kThreads)
+template <int kRowWarps, int kM, int kStages, bool kFp8, bool kRagged>
+__global__ void __launch_bounds__(kThreads, kM == 1 ? 3 : 2)
 linear_w4_kernel(const W4Params p) {
-  using S = W4Shape<kRowWarps, kTiles>;
+  using S = W4Shape<kRowWarps, kM, kStages>;
   using Vec = std::conditional_t<kFp8, uint2, uint4>;  // 8 values of x
   extern __shared__ __align__(16) uint8_t smem[];
   float* part = reinterpret_cast<float*>(smem);
+  constexpr int kElem = kFp8 ? 1 : 2;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lg = lane >> 2, lt = lane & 3;
   const int rw = warp % kRowWarps, kw = warp / kRowWarps;
   const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
-  const int n0 = tile * S::kRows;
-  const int t0 = blockIdx.z * S::kTok;
+  const int n0 = tile * S::kRows, rw0 = rw * 16 * kM;
+  const int t0 = blockIdx.z * kTok;
   const int g0 = rank * p.per + kw, g1 = min(p.groups, rank * p.per + p.per);
+  const int ragged = kRagged ? p.groups - 1 : -1;  // the group with 64 columns, if any
   if (!p.early) grid_dep_wait();
 
-  const int r0 = n0 + rw * 16 + lg;
+  // Rows past N are read as the last one: their sums are not stored.
   const int64_t row_bytes = p.K >> 1;
-  const uint8_t* src0 = p.w4 + static_cast<int64_t>(r0) * row_bytes + lt * 16;
-  const bool in0 = r0 < p.N, in1 = r0 + 8 < p.N;
-  const uint32_t ring = smem_u32(smem) + warp * 1024;
-  const uint32_t sw_off = (lg >> 1 & 3) << 4;  // the row's 16-byte unit permutation
-  const uint32_t put = ring + lg * 64 + ((lt << 4) ^ sw_off);
-  const uint32_t get = ring + lg * 64 + lt * 4;
+  const uint8_t* src[2 * kM];
+  int sw_at[2 * kM];
+#pragma unroll
+  for (int m = 0; m < 2 * kM; ++m) {
+    const int r = min(n0 + rw0 + 8 * m + lg, p.N - 1);
+    src[m] = p.w4 + r * row_bytes + g0 * 64 + lt * 16;
+    sw_at[m] = r * p.groups;
+  }
+  const uint32_t ring = smem_u32(smem) + warp * (kM * 1024) + lg * 64;
+  const uint32_t perm = (lg >> 1 & 3) << 4;  // the row's 16-byte units lie at unit ^ (row / 2 % 4)
+  const uint32_t put = ring + ((lt << 4) ^ perm);
+  uint32_t get[4];  // word 4 j + t of row g
+#pragma unroll
+  for (int j = 0; j < 4; ++j) get[j] = ring + ((j << 4) ^ perm) + lt * 4;
   auto fetch = [&](int g, int stage) {
-    // K is a multiple of 64: the last group may have only two of its four 16-byte units
-    const int64_t at = static_cast<int64_t>(g) * 64;
-    const bool inside = g < g1 && at + lt * 16 < row_bytes;
-    const bool a = inside && in0, b = inside && in1;
-    const uint32_t dst = put + stage * (kWarps * 1024);
-    cp_async16_zfill(dst, a ? src0 + at : p.w4, a ? 16u : 0u);
-    cp_async16_zfill(dst + 512, b ? src0 + 8 * row_bytes + at : p.w4, b ? 16u : 0u);
+    if (g < g1) {
+      // past the 64 columns of a ragged group: its first units again, which meet zeros of x
+      const int back = kRagged && g == ragged && lt >= 2 ? 32 : 0;
+#pragma unroll
+      for (int m = 0; m < 2 * kM; ++m) {
+        cp_async16(put + stage * S::kStage + m * 512, src[m] - back);
+        src[m] += S::kKWarps * 64;
+      }
+    }
     cp_async_commit();
   };
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(g0 + s * S::kKWarps, s);
+  // The weights' scales are two bytes here and there: lane (g, t) loads those of its rows for step t of the next
+  // four, four steps ahead, and a shuffle hands them round.
+  uint16_t sw[2 * kM], next_sw[2 * kM];
+  auto load_sw = [&](int step) {
+    const int g = min(g0 + (step + lt) * S::kKWarps, p.groups - 1);
+#pragma unroll
+    for (int m = 0; m < 2 * kM; ++m) next_sw[m] = p.sw[sw_at[m] + g];
+  };
+  load_sw(0);
   if (p.early) grid_dep_wait();
   grid_dep_launch();
 
-  auto load = [&](int g, W4Operands<kTiles, kFp8>& o) {
-    if (g >= g1) return;
+  // Columns past T repeat the last token: their sums are not stored.
+  const uint8_t* x_at =
+      static_cast<const uint8_t*>(p.x) + (static_cast<int64_t>(min(t0 + lg, p.T - 1)) * p.K + 8 * lt) * kElem;
+  const int sx_at[2] = {min(t0 + 2 * lt, p.T - 1) * p.groups, min(t0 + 2 * lt + 1, p.T - 1) * p.groups};
+  Vec next_x[4];
+  float next_sx[2] = {1.f, 1.f};
+  auto load_x = [&](int g) {
+    g = min(g, g1 - 1);  // past the last group: loaded again, not used
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int t = t0 + 8 * i + lg;
-      const Vec* row = reinterpret_cast<const Vec*>(static_cast<const uint8_t*>(p.x) +
-                                                    (static_cast<int64_t>(t) * p.K + g * kW4Group) * (kFp8 ? 1 : 2));
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o.x[i][j] = t < p.T && g * kW4Group + 8 * (4 * j + lt) < p.K ? row[4 * j + lt] : Vec{};
-      if (kFp8) {
-        const int c = t0 + 8 * i + 2 * lt;
-        o.sx[i][0] = c < p.T ? p.sx[static_cast<int64_t>(c) * p.groups + g] : 0.f;
-        o.sx[i][1] = c + 1 < p.T ? p.sx[static_cast<int64_t>(c + 1) * p.groups + g] : 0.f;
-      }
+    for (int j = 0; j < 4; ++j)
+      next_x[j] = j < 2 || g != ragged
+                      ? *reinterpret_cast<const Vec*>(x_at + static_cast<int64_t>(g) * (kW4Group * kElem) + j * 32 * kElem)
+                      : Vec{};
+    if (kFp8) {
+      next_sx[0] = p.sx[sx_at[0] + g];
+      next_sx[1] = p.sx[sx_at[1] + g];
     }
-    o.sw[0] = in0 ? bf16_bits_to_f32(p.sw[static_cast<int64_t>(r0) * p.groups + g]) : 0.f;
-    o.sw[1] = in1 ? bf16_bits_to_f32(p.sw[static_cast<int64_t>(r0 + 8) * p.groups + g]) : 0.f;
   };
 
-  float acc[kTiles][4];
+  float acc[kM][4];
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  W4Operands<kTiles, kFp8> next;
-  load(g0, next);
-  int stage = 0;
-  for (int g = g0; g < g1; g += S::kKWarps) {
-    const W4Operands<kTiles, kFp8> o = next;
-    load(g + S::kKWarps, next);
-    cp_async_wait_group<kStages - 2>();
-    __syncwarp();  // the group has landed for every lane, and every lane has read the one before
-    fetch(g + (kStages - 1) * S::kKWarps, stage == 0 ? kStages - 1 : stage - 1);
-    const uint32_t at = get + stage * (kWarps * 1024);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-
-    float sum[kTiles][4];
+  for (int i = 0; i < kM; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  if (g0 < g1) load_x(g0);
+  static_assert(kStages == 4, "the ring's slot is the step within four");
+  for (int g = g0, step = 0; g < g1; step += 4) {
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
+    for (int m = 0; m < 2 * kM; ++m) sw[m] = next_sw[m];
+    load_sw(step + 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t unit = (j << 4) ^ sw_off;
-      const uint32_t va = ld_shared_u32(at + unit), vb = ld_shared_u32(at + 512 + unit);
-      uint32_t a[4], b[4];
-      if (kFp8) {
-        w4_pairs_f16(va, a);
-        w4_pairs_f16(vb, b);
-      } else {
-        w4_pairs(va, a);
-        w4_pairs(vb, b);
-      }
+    for (int q = 0; q < 4; ++q, g += S::kKWarps) {
+      if (g >= g1) break;
+      uint4 x[4];
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        uint32_t x[4];
-        pair_order(o.x[i][j], x);
-        mma_16816<kFp8>(sum[i], a[0], b[0], a[1], b[1], x[0], x[1]);
-        mma_16816<kFp8>(sum[i], a[2], b[2], a[3], b[3], x[2], x[3]);
+      for (int j = 0; j < 4; ++j) x[j] = pair_order(next_x[j]);
+      const float sx[2] = {next_sx[0], next_sx[1]};
+      load_x(g + S::kKWarps);
+      cp_async_wait_group<kStages - 2>();
+      __syncwarp();  // the group has landed for every lane, and every lane has read the one before
+      fetch(g + (kStages - 1) * S::kKWarps, (q + 3) & 3);
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        float sum[2][4];  // two chains of MMAs
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t at = get[j] + q * S::kStage + i * 1024;
+          const uint32_t va = ld_shared_u32(at), vb = ld_shared_u32(at + 512);
+          uint32_t a[4], b[4];
+          if (kFp8) {
+            w4_pairs_f16(va, a);
+            w4_pairs_f16(vb, b);
+          } else {
+            w4_pairs(va, a);
+            w4_pairs(vb, b);
+          }
+          if (j == 0) {
+            mma_16816<kFp8, true>(sum[0], a[0], b[0], a[1], b[1], x[j].x, x[j].y);
+            mma_16816<kFp8, true>(sum[1], a[2], b[2], a[3], b[3], x[j].z, x[j].w);
+          } else {
+            mma_16816<kFp8, false>(sum[0], a[0], b[0], a[1], b[1], x[j].x, x[j].y);
+            mma_16816<kFp8, false>(sum[1], a[2], b[2], a[3], b[3], x[j].z, x[j].w);
+          }
+        }
+        const float s[2] = {
+            bf16_bits_to_f32(__shfl_sync(0xffffffffu, static_cast<int>(sw[2 * i]), (lane & 28) | q)),
+            bf16_bits_to_f32(__shfl_sync(0xffffffffu, static_cast<int>(sw[2 * i + 1]), (lane & 28) | q))};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = sum[0][e] + sum[1][e];
+          if (kFp8) v *= sx[e & 1];
+          acc[i][e] = fmaf(v, s[e >> 1], acc[i][e]);
+        }
       }
     }
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = kFp8 ? sum[i][e] * o.sx[i][e & 1] : sum[i][e];
-        acc[i][e] = fmaf(v, o.sw[e >> 1], acc[i][e]);
-      }
   }
   cp_async_wait_all();
   __syncthreads();  // the ring is done with: the partials take its place
 
   // partial [K warp][token][row]
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i)
+  for (int i = 0; i < kM; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int t = i * 8 + lt * 2 + (e & 1), r = rw * 16 + lg + (e >> 1) * 8;
-      part[(kw * S::kTok + t) * S::kLd + r] = acc[i][e];
+      const int t = lt * 2 + (e & 1), r = rw0 + i * 16 + lg + (e >> 1) * 8;
+      part[(kw * kTok + t) * S::kLd + r] = acc[i][e];
     }
   if (p.split > 1) cluster_sync();
   else __syncthreads();
 
   // the cluster's threads share the (token, row) sums, row fastest, each in rank and warp order
-  const int toks = min(S::kTok, p.T - t0);
+  const int toks = min(kTok, p.T - t0);
   const uint32_t base = smem_u32(part);
   for (int e = rank * kThreads + tid; e < toks * S::kRows; e += p.split * kThreads) {
     const int r = e % S::kRows, t = e / S::kRows;
@@ -252,29 +274,29 @@ linear_w4_kernel(const W4Params p) {
     for (int q = 0; q < p.split; ++q) {
       const uint32_t at = p.split > 1 ? mapa(base, q) : base;
 #pragma unroll
-      for (int k = 0; k < S::kKWarps; ++k) v += ld_cluster_f32(at + ((k * S::kTok + t) * S::kLd + r) * 4);
+      for (int k = 0; k < S::kKWarps; ++k) v += ld_cluster_f32(at + ((k * kTok + t) * S::kLd + r) * 4);
     }
     p.y[static_cast<int64_t>(t0 + t) * p.N + n0 + r] = f32_to_bf16_bits(v);
   }
   if (p.split > 1) cluster_sync();  // peers may still be reading this CTA's partial
 }
 
-template <int kRowWarps, int kTiles, bool kFp8>
+template <int kRowWarps, int kM, int kStages, bool kFp8, bool kRagged>
 cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
-  using S = W4Shape<kRowWarps, kTiles>;
+  using S = W4Shape<kRowWarps, kM, kStages>;
   static bool configured[kMaxDevicesLocal] = {};  // the attribute is per device
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
-  auto kernel = linear_w4_kernel<kRowWarps, kTiles, kFp8>;
+  auto kernel = linear_w4_kernel<kRowWarps, kM, kStages, kFp8, kRagged>;
   if (!configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kRing);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
   const int tiles = (p.N + S::kRows - 1) / S::kRows;
   p.split = 1;
   while (p.split < kMaxSplit && tiles * p.split < 304 && p.groups >= 2 * p.split * S::kKWarps) p.split *= 2;
-  if (getenv("W4_SPLIT")) p.split = atoi(getenv("W4_SPLIT"));
+  if (getenv("W4_SPLIT") && atoi(getenv("W4_SPLIT"))) p.split = atoi(getenv("W4_SPLIT"));
   p.early = launch_overlap() >= 2;
   p.per = (p.groups + p.split - 1) / p.split;
   cudaLaunchAttribute attr[2];
@@ -284,29 +306,32 @@ cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * p.split, 1, (p.T + S::kTok - 1) / S::kTok);
+  cfg.gridDim = dim3(tiles * p.split, 1, (p.T + kTok - 1) / kTok);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.dynamicSmemBytes = S::kRing;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_overlap() > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <bool kFp8, int kTiles>
-cudaError_t launch_rw(const W4Params& p, cudaStream_t stream) {
+template <bool kFp8, int kM, int kStages>
+cudaError_t launch_a(const W4Params& p, cudaStream_t stream) {
   const int rw = getenv("W4_RW") ? atoi(getenv("W4_RW")) : 4;
-  if (rw == 1) return launch_shape<1, kTiles, kFp8>(p, stream);
-  if (rw == 2) return launch_shape<2, kTiles, kFp8>(p, stream);
-  if (rw == 4) return launch_shape<4, kTiles, kFp8>(p, stream);
-  return launch_shape<8, kTiles, kFp8>(p, stream);
+  if (p.K % kW4Group) {
+    if (rw == 1) return launch_shape<1, kM, kStages, kFp8, true>(p, stream);
+    return launch_shape<4, kM, kStages, kFp8, true>(p, stream);
+  }
+  if (rw == 1) return launch_shape<1, kM, kStages, kFp8, false>(p, stream);
+  if (rw == 2) return launch_shape<2, kM, kStages, kFp8, false>(p, stream);
+  if (rw == 4) return launch_shape<4, kM, kStages, kFp8, false>(p, stream);
+  return launch_shape<8, kM, kStages, kFp8, false>(p, stream);
 }
-
 template <bool kFp8>
 cudaError_t launch_any(const W4Params& p, cudaStream_t stream) {
-  if (p.T <= 8) return launch_rw<kFp8, 1>(p, stream);
-  if (p.T <= 16) return launch_rw<kFp8, 2>(p, stream);
-  return launch_rw<kFp8, 4>(p, stream);
+  const int m = getenv("W4_M") ? atoi(getenv("W4_M")) : 1;
+  if (m == 1) return launch_a<kFp8, 1, 4>(p, stream);
+  return launch_a<kFp8, 2, 4>(p, stream);
 }
 
 }  // namespace
