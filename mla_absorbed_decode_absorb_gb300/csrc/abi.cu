@@ -380,14 +380,20 @@ mla_status mla_dequantize_w4(const uint8_t* w4, const mla_bf16* w_scale, mla_bf1
 mla_status mla_linear_w4(const mla_bf16* x, const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* y, int T, int K,
                          int N, cudaStream_t stream) {
   const mla_status s = linear_w4_check(x, 2, nullptr, w4, w_scale, y, T, K, N);
-  return s != MLA_OK ? s : from_cuda(launch_linear_w4(x, nullptr, w4, w_scale, y, T, K, N, stream));
+  if (s != MLA_OK) return s;
+  int* st = status_ptr();
+  if (st == nullptr) return MLA_ERR_CUDA;
+  return from_cuda(launch_linear_w4(x, nullptr, w4, w_scale, y, T, K, N, st, stream));
 }
 
 mla_status mla_linear_w4_fp8(const uint8_t* x8, const float* x_scale, const uint8_t* w4, const mla_bf16* w_scale,
                              mla_bf16* y, int T, int K, int N, cudaStream_t stream) {
   if (!x_scale || !aligned16(x_scale)) return MLA_ERR_INVALID_ARG;
   const mla_status s = linear_w4_check(x8, 1, x_scale, w4, w_scale, y, T, K, N);
-  return s != MLA_OK ? s : from_cuda(launch_linear_w4(x8, x_scale, w4, w_scale, y, T, K, N, stream));
+  if (s != MLA_OK) return s;
+  int* st = status_ptr();
+  if (st == nullptr) return MLA_ERR_CUDA;
+  return from_cuda(launch_linear_w4(x8, x_scale, w4, w_scale, y, T, K, N, st, stream));
 }
 
 mla_status mla_read_kv_fp8(const uint8_t* cache_c8, const float* cache_scale, const uint16_t* cache_kr,

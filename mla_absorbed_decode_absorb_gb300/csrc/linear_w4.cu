@@ -39,18 +39,7 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxSplit = 8;       // CTAs of a cluster along K (the portable size)
 
-struct W4Params {
-  const void* x;        // bf16 [T, K] or E4M3 [T, K]
-  const float* sx;      // [T, groups] (E4M3 x)
-  const uint8_t* w4;    // [N, K / 2]
-  const uint16_t* sw;   // [N, groups] bf16
-  uint16_t* y;          // [T, N] bf16
-  int T, K, N, groups;
-  int split, per;       // CTAs along K, groups per CTA
-  bool early;           // the weights may be read before the previous kernel has finished
-};
 
 // c (+)= a b; with kFirst, c = a b.
 template <bool kF16, bool kFirst>
@@ -75,33 +64,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 #undef MLA_MMA_16816
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// Two E4M3 codes (the low 16 bits) as an f16 pair, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
-  return h;
-}
-
-// Eight values of x, as loaded, as MMA operands in the pair order (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ uint4 pair_order(const uint4& v) {
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                    __byte_perm(v.y, v.w, 0x7632));
-}
-__device__ __forceinline__ uint4 pair_order(const uint2& v) {
-  const uint32_t a = __byte_perm(v.x, v.y, 0x5140), c = __byte_perm(v.x, v.y, 0x7362);
-  return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(c), e4m3x2_to_f16x2(c >> 16));
-}
-
 constexpr int kTok = 8;  // tokens of a CTA: the columns of one MMA
 
 // kRowWarps warps cover 16 kM rows each, the other kWarps / kRowWarps share their groups of K.
@@ -295,24 +262,11 @@ cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
   }
   const int tiles = (p.N + S::kRows - 1) / S::kRows;
   p.split = 1;
-  while (p.split < kMaxSplit && tiles * p.split < 304 && p.groups >= 2 * p.split * S::kKWarps) p.split *= 2;
+  while (p.split < kW4MaxSplit && tiles * p.split < 304 && p.groups >= 2 * p.split * S::kKWarps) p.split *= 2;
   if (getenv("W4_SPLIT") && atoi(getenv("W4_SPLIT"))) p.split = atoi(getenv("W4_SPLIT"));
   p.early = launch_overlap() >= 2;
   p.per = (p.groups + p.split - 1) / p.split;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * p.split, 1, (p.T + kTok - 1) / kTok);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kRing;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = launch_overlap() > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return launch_w4(kernel, dim3(tiles * p.split, 1, (p.T + kTok - 1) / kTok), kThreads, S::kRing, stream, p);
 }
 
 template <bool kFp8, int kM, int kStages>
@@ -337,8 +291,10 @@ cudaError_t launch_any(const W4Params& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_linear_w4(const void* x, const float* x_scale, const uint8_t* w4, const uint16_t* w_scale,
-                             uint16_t* y, int T, int K, int N, cudaStream_t stream) {
-  W4Params p{x, x_scale, w4, w_scale, y, T, K, N, w4_groups(K), 1, 0, false};
+                             uint16_t* y, int T, int K, int N, int* status, cudaStream_t stream) {
+  W4Params p{x, x_scale, w4, w_scale, y, status, T, K, N, w4_groups(K), 1, 0, false};
+  const int lim = getenv("W4_LIM") ? atoi(getenv("W4_LIM")) : 8;
+  if (T > lim) return launch_linear_w4_tc(p, stream);
   return x_scale != nullptr ? launch_any<true>(p, stream) : launch_any<false>(p, stream);
 }
 

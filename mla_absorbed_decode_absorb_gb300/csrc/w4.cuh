@@ -5,6 +5,8 @@
 // one bf16 scale s for each 128 columns.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "internal.cuh"
 
 namespace mla {
@@ -43,5 +45,64 @@ __device__ __forceinline__ void w4_pairs_f16(uint32_t v, uint32_t (&p)[4]) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[2 * i + 1]) : "r"(hi), "r"(0x2c002c00u), "r"(0xd480d480u));  // / 16 - 72
   }
 }
+
+// ------------------------------------------------------------------ projections
+constexpr int kW4MaxSplit = 8;  // CTAs of a cluster along K (the portable size)
+
+struct W4Params {
+  const void* x;        // bf16 [T, K] or E4M3 [T, K]
+  const float* sx;      // [T, groups] (E4M3 x)
+  const uint8_t* w4;    // [N, K / 2]
+  const uint16_t* sw;   // [N, groups] bf16
+  uint16_t* y;          // [T, N] bf16
+  int* status;
+  int T, K, N, groups;
+  int split, per;       // CTAs along K, groups per CTA
+  bool early;           // the weights may be read before the previous kernel has finished
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Two E4M3 codes (the low 16 bits) as an f16 pair, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  return h;
+}
+
+// Eight values of x, as loaded, as MMA operands in the pair order (0,4) (1,5) (2,6) (3,7).
+__device__ __forceinline__ uint4 pair_order(const uint4& v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
+}
+__device__ __forceinline__ uint4 pair_order(const uint2& v) {
+  const uint32_t a = __byte_perm(v.x, v.y, 0x5140), c = __byte_perm(v.x, v.y, 0x7362);
+  return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(c), e4m3x2_to_f16x2(c >> 16));
+}
+
+// The launch of a projection kernel: clusters of p.split CTAs along x.
+template <typename Kernel>
+cudaError_t launch_w4(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const W4Params& p) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = launch_overlap() > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// More than a few tokens (csrc/linear_w4_tc.cu).
+cudaError_t launch_linear_w4_tc(const W4Params& p, cudaStream_t stream);
 
 }  // namespace mla
