@@ -462,7 +462,7 @@ mla_status mla_prefill_attn(const mla_bf16* q_nope, const mla_bf16* q_rope, cons
  *   v = h / sqrt(mean(h^2) + eps) * weight
  *   y = bf16(v)
  *   y_scale[t, g] = s = max(max|v| / 448, 2^-100) over columns [128 g, 128 g + 128)
- *   y8 = E4M3(v * (1 / s)), nearest even
+ *   y8 = E4M3(v / s), nearest even
  * h, its sum of squares and v are float32 (h is not rounded before the norm).
  *   x            [T, D] bf16, row t at x + t * x_ld (x_ld >= D, a multiple of 8)
  *   residual     [T, D] bf16 (nullable, with residual_out)
@@ -501,9 +501,11 @@ mla_status mla_rms_norm(const mla_bf16* x, int64_t x_ld, const mla_bf16* residua
  * applied to each group's sum in float32, and y is rounded once.  K is split
  * over the CTAs of a cluster, whose partials are added in a fixed order on
  * chip: no workspace, and a result that does not depend on timing.
- * N >= 1, K >= 64 a multiple of 64; y must not overlap an input.
+ * N >= 1, K >= 64 a multiple of 64; the projections take K <= MLA_W4_MAX_K
+ * (MLA_ERR_UNSUPPORTED beyond); y must not overlap an input.
  */
 #define MLA_W4_GROUP 128
+#define MLA_W4_MAX_K 4194304
 mla_status mla_quantize_w4(const mla_bf16* w, uint8_t* w4, mla_bf16* w_scale, int N, int K, cudaStream_t stream);
 mla_status mla_dequantize_w4(const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* w, int N, int K,
                              cudaStream_t stream);

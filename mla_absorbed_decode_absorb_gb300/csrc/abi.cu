@@ -79,6 +79,7 @@ mla_status linear_w4_check(const void* x, int x_elem, const float* x_scale, cons
   if (T < 1 || T > MLA_LINEAR_MAX_T) return MLA_ERR_INVALID_ARG;
   const mla_status s = w4_check(w4, w_scale, N, K);
   if (s != MLA_OK) return s;
+  if (K > MLA_W4_MAX_K) return MLA_ERR_UNSUPPORTED;  // x is indexed in 32 bits
   if (!x || !y || !aligned16(x) || (reinterpret_cast<uintptr_t>(y) & 1u) != 0) return MLA_ERR_INVALID_ARG;
   const Range out{y, static_cast<size_t>(T) * N * 2};
   const size_t groups = (static_cast<size_t>(K) + MLA_W4_GROUP - 1) / MLA_W4_GROUP;

@@ -25,8 +25,6 @@
 // distributed shared memory, so a call needs no workspace and its result does not
 // depend on timing.
 #include <cuda_fp16.h>
-#include <stdlib.h>
-
 #include <type_traits>
 
 #include "sm100.cuh"
@@ -39,7 +37,9 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-
+constexpr int kTok = 8;        // tokens of a CTA: the columns of one MMA
+constexpr int kStages = 4;     // groups a warp has in flight or in use, kM KB each
+constexpr int kOneWave = 456;  // CTAs of 16 rows that are resident at once (152 SMs, three each)
 
 // c (+)= a b; with kFirst, c = a b.
 template <bool kF16, bool kFirst>
@@ -69,10 +69,9 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-constexpr int kTok = 8;  // tokens of a CTA: the columns of one MMA
 
 // kRowWarps warps cover 16 kM rows each, the other kWarps / kRowWarps share their groups of K.
-template <int kRowWarps, int kM, int kStages>
+template <int kRowWarps, int kM>
 struct W4Shape {
   static constexpr int kKWarps = kWarps / kRowWarps;
   static constexpr int kRows = 16 * kM * kRowWarps;
@@ -82,10 +81,10 @@ struct W4Shape {
   static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
 };
 
-template <int kRowWarps, int kM, int kStages, bool kFp8, bool kRagged>
+template <int kRowWarps, int kM, bool kFp8, bool kRagged>
 __global__ void __launch_bounds__(kThreads, kM == 1 ? 3 : 2)
 linear_w4_kernel(const W4Params p) {
-  using S = W4Shape<kRowWarps, kM, kStages>;
+  using S = W4Shape<kRowWarps, kM>;
   using Vec = std::conditional_t<kFp8, uint2, uint4>;  // 8 values of x
   extern __shared__ __align__(16) uint8_t smem[];
   float* part = reinterpret_cast<float*>(smem);
@@ -166,7 +165,7 @@ linear_w4_kernel(const W4Params p) {
 #pragma unroll
   for (int i = 0; i < kM; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   if (g0 < g1) load_x(g0);
-  static_assert(kStages == 4, "the ring's slot is the step within four");
+  static_assert(kStages == 4, "a ring slot is a step within the four of the loop");
   for (int g = g0, step = 0; g < g1; step += 4) {
 #pragma unroll
     for (int m = 0; m < 2 * kM; ++m) sw[m] = next_sw[m];
@@ -228,74 +227,85 @@ linear_w4_kernel(const W4Params p) {
       const int t = lt * 2 + (e & 1), r = rw0 + i * 16 + lg + (e >> 1) * 8;
       part[(kw * kTok + t) * S::kLd + r] = acc[i][e];
     }
-  if (p.split > 1) cluster_sync();
-  else __syncthreads();
+  if (S::kKWarps > 1 || p.split == 1) __syncthreads();
+  else cluster_sync();
 
-  // the cluster's threads share the (token, row) sums, row fastest, each in rank and warp order
   const int toks = min(kTok, p.T - t0);
+  if (S::kKWarps > 1) {
+    // this CTA's K warps in order, into the first one's place
+    for (int e = tid; e < toks * S::kRows; e += kThreads) {
+      float* at = part + (e / S::kRows) * S::kLd + e % S::kRows;
+      float v = at[0];
+#pragma unroll
+      for (int k = 1; k < S::kKWarps; ++k) v += at[k * kTok * S::kLd];
+      at[0] = v;
+    }
+    if (p.split > 1) cluster_sync();
+    else __syncthreads();
+  }
+
+  // the cluster's threads share the (token, row) sums, row fastest, each in rank order
   const uint32_t base = smem_u32(part);
   for (int e = rank * kThreads + tid; e < toks * S::kRows; e += p.split * kThreads) {
     const int r = e % S::kRows, t = e / S::kRows;
     if (n0 + r >= p.N) continue;
-    float v = 0.f;
-    for (int q = 0; q < p.split; ++q) {
-      const uint32_t at = p.split > 1 ? mapa(base, q) : base;
-#pragma unroll
-      for (int k = 0; k < S::kKWarps; ++k) v += ld_cluster_f32(at + ((k * kTok + t) * S::kLd + r) * 4);
-    }
+    const float v = sum_partials(base + (t * S::kLd + r) * 4, p.split);
     p.y[static_cast<int64_t>(t0 + t) * p.N + n0 + r] = f32_to_bf16_bits(v);
   }
   if (p.split > 1) cluster_sync();  // peers may still be reading this CTA's partial
 }
 
-template <int kRowWarps, int kM, int kStages, bool kFp8, bool kRagged>
+template <int kRowWarps, int kM, bool kFp8, bool kRagged>
 cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
-  using S = W4Shape<kRowWarps, kM, kStages>;
+  using S = W4Shape<kRowWarps, kM>;
   static bool configured[kMaxDevicesLocal] = {};  // the attribute is per device
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
-  auto kernel = linear_w4_kernel<kRowWarps, kM, kStages, kFp8, kRagged>;
+  auto kernel = linear_w4_kernel<kRowWarps, kM, kFp8, kRagged>;
   if (!configured[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kRing);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  const int tiles = (p.N + S::kRows - 1) / S::kRows;
+  const int tiles = (p.N + S::kRows - 1) / S::kRows, slices = (p.T + kTok - 1) / kTok;
+  // K over a cluster while its CTAs still fit the GPU at once and a warp keeps more than one group (7168 -> 576, one
+  // token: 3.6 us in four, against 4.8 undivided and 3.7 in eight)
   p.split = 1;
-  while (p.split < kW4MaxSplit && tiles * p.split < 304 && p.groups >= 2 * p.split * S::kKWarps) p.split *= 2;
-  if (getenv("W4_SPLIT") && atoi(getenv("W4_SPLIT"))) p.split = atoi(getenv("W4_SPLIT"));
-  p.early = launch_overlap() >= 2;
+  if (kM == 1)
+    while (p.split < kW4MaxSplit && tiles * slices * p.split * 2 <= kOneWave && 2 * p.groups >= 3 * S::kKWarps * 2 * p.split)
+      p.split *= 2;
   p.per = (p.groups + p.split - 1) / p.split;
-  return launch_w4(kernel, dim3(tiles * p.split, 1, (p.T + kTok - 1) / kTok), kThreads, S::kRing, stream, p);
+  p.early = launch_overlap() >= 2;
+  return launch_w4(kernel, dim3(tiles * p.split, 1, (p.T + kTok - 1) / kTok), kThreads, S::kRing, stream, p.split, p);
 }
 
-template <bool kFp8, int kM, int kStages>
-cudaError_t launch_a(const W4Params& p, cudaStream_t stream) {
-  const int rw = getenv("W4_RW") ? atoi(getenv("W4_RW")) : 4;
-  if (p.K % kW4Group) {
-    if (rw == 1) return launch_shape<1, kM, kStages, kFp8, true>(p, stream);
-    return launch_shape<4, kM, kStages, kFp8, true>(p, stream);
-  }
-  if (rw == 1) return launch_shape<1, kM, kStages, kFp8, false>(p, stream);
-  if (rw == 2) return launch_shape<2, kM, kStages, kFp8, false>(p, stream);
-  if (rw == 4) return launch_shape<4, kM, kStages, kFp8, false>(p, stream);
-  return launch_shape<8, kM, kStages, kFp8, false>(p, stream);
-}
-template <bool kFp8>
-cudaError_t launch_any(const W4Params& p, cudaStream_t stream) {
-  const int m = getenv("W4_M") ? atoi(getenv("W4_M")) : 1;
-  if (m == 1) return launch_a<kFp8, 1, 4>(p, stream);
-  return launch_a<kFp8, 2, 4>(p, stream);
+template <int kRowWarps, int kM>
+cudaError_t launch_rows(const W4Params& p, cudaStream_t stream) {
+  const bool ragged = p.K % kW4Group != 0;
+  if (p.sx != nullptr)
+    return ragged ? launch_shape<kRowWarps, kM, true, true>(p, stream) : launch_shape<kRowWarps, kM, true, false>(p, stream);
+  return ragged ? launch_shape<kRowWarps, kM, false, true>(p, stream) : launch_shape<kRowWarps, kM, false, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_w4(const void* x, const float* x_scale, const uint8_t* w4, const uint16_t* w_scale,
                              uint16_t* y, int T, int K, int N, int* status, cudaStream_t stream) {
-  W4Params p{x, x_scale, w4, w_scale, y, status, T, K, N, w4_groups(K), 1, 0, false};
-  const int lim = getenv("W4_LIM") ? atoi(getenv("W4_LIM")) : 8;
-  if (T > lim) return launch_linear_w4_tc(p, stream);
-  return x_scale != nullptr ? launch_any<true>(p, stream) : launch_any<false>(p, stream);
+  const W4Params p{x, x_scale, w4, w_scale, y, status, T, K, N, w4_groups(K), 1, 0, false};
+  const int slices = (T + kTok - 1) / kTok;
+  const int64_t tiles = static_cast<int64_t>((N + 15) / 16) * slices;
+  // Warp MMAs pass over the weights once for 8 tokens, the tensor-core kernel once for 16 to 64 but with a longer way
+  // from weight to result: it wins from two passes on once they are over about 36 M weights (1536 x 16384: 17 tokens
+  // 11.2 us against 12.8, 16 tokens 9.9 against 9.5; 16384 x 7168: 16 tokens 26 against 32, 64 tokens 33 against
+  // 94; but 7168 x 576: 64 tokens 9.8 against 7.4, 512 x 512: 7.1 against 2.4).
+  if (slices > 1 && static_cast<int64_t>(N) * K * slices > 36000000) return launch_linear_w4_tc(p, stream);
+  // Up to one wave of CTAs, 16 rows each and K over all eight warps: the latency of few, short streams counts.
+  // Beyond, 32 rows a warp share what it unpacks of x (1536 -> 16384, one token: 6.6 us against 7.4), and fewer warps
+  // share K where it is short.
+  if (tiles <= kOneWave) return launch_rows<1, 1>(p, stream);
+  if (p.groups >= 48) return launch_rows<1, 2>(p, stream);
+  if (p.groups >= 4) return launch_rows<2, 2>(p, stream);
+  return launch_rows<8, 2>(p, stream);
 }
 
 }  // namespace mla

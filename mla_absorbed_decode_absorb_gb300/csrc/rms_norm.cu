@@ -10,8 +10,7 @@
 // formula needs (the sum of squares, then the scaling), so x and r are read
 // once.  The sum, h and y stay in fp32: y comes from the unrounded h, and each
 // output is rounded once.  A group of 128 columns is 16 neighbouring lanes of 8
-// columns each, so its maximum is four shuffles, and its codes are v * (1 / s),
-// one IEEE division per group.  Bound by HBM for many rows, by the launch and one
+// columns each, so its maximum is four shuffles.  Bound by HBM for many rows, by the launch and one
 // round trip to memory for few (1 x 7168: 1.9 us).
 #include "append_row.cuh"
 
@@ -57,8 +56,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // neighbouring lanes always hold one whole group of 128 columns.  kSpan = 32: a
 // warp per row, kThreads / 32 rows per CTA; otherwise one row per CTA, which may
 // have fewer threads than kThreads (kSpan = 0).
+// (Threads of one or two chunks are held to 32 registers, which keeps an SM's 2048 threads in flight.)
 template <int kChunks, int kThreads, int kSpan>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kChunks <= 2 && kSpan == 0 ? 2048 / kThreads : 1)
 rms_norm_kernel(const NormParams p) {
   __shared__ float warp_sum[kSpan == 32 ? 1 : 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -115,20 +115,29 @@ rms_norm_kernel(const NormParams p) {
     const int c = tid + i * span;
     float w[8];
     unpack8(c < chunks ? reinterpret_cast<const uint4*>(p.w)[c] : make_uint4(0, 0, 0, 0), w);
+    if (p.y != nullptr && c < chunks) {
+      float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * inv * w[e];
-    if (p.y != nullptr && c < chunks) reinterpret_cast<uint4*>(p.y)[base + c] = pack8(h[i]);
+      for (int e = 0; e < 8; ++e) v[e] = h[i][e] * inv * w[e];
+      reinterpret_cast<uint4*>(p.y)[base + c] = pack8(v);
+    }
     if (p.y8 != nullptr) {
+      // v / s = h w * (448 / max|h w|): the row's factor cancels, and with it its rounding
       float a = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(h[i][e]));
+      for (int e = 0; e < 8; ++e) {
+        h[i][e] *= w[e];
+        a = fmaxf(a, fabsf(h[i][e]));
+      }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      const float s = fmaxf(__fdiv_rn(a, 448.f), kScaleFloor);
-      const float rs = __fdiv_rn(1.f, s);
+      const float s = fmaxf(__fdiv_rn(a * inv, 448.f), kScaleFloor);
+      // at the floor (also where the row is not finite, or a is 0) the codes are v / 2^-100
+      const bool at_floor = s == kScaleFloor;
+      const float f = at_floor ? inv : __fdiv_rn(448.f, a), g = at_floor ? 0x1p100f : 1.f;
       uint16_t q[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = e4m3x2(h[i][2 * e] * rs, h[i][2 * e + 1] * rs);
+      for (int e = 0; e < 4; ++e) q[e] = e4m3x2(h[i][2 * e] * f * g, h[i][2 * e + 1] * f * g);
       if (c < chunks) {
         reinterpret_cast<uint2*>(p.y8)[base + c] =
             make_uint2(q[0] | (static_cast<uint32_t>(q[1]) << 16), q[2] | (static_cast<uint32_t>(q[3]) << 16));

@@ -7,7 +7,7 @@
 
 #include <cuda_fp16.h>
 
-#include "internal.cuh"
+#include "sm100.cuh"
 
 namespace mla {
 
@@ -66,29 +66,48 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-// Two E4M3 codes (the low 16 bits) as an f16 pair, exact.
+// The float at shared address `at` of every CTA of the cluster, added in rank order (all loads in flight together).
+__device__ __forceinline__ float sum_partials(uint32_t at, int split) {
+  float v[kW4MaxSplit];
+  if (split == 1) {
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(at) : "memory");
+    return v[0];
+  }
+#pragma unroll
+  for (int q = 0; q < kW4MaxSplit; ++q) v[q] = q < split ? ld_cluster_f32(sm100::mapa(at, q)) : 0.f;
+  float sum = v[0];
+#pragma unroll
+  for (int q = 1; q < kW4MaxSplit; ++q) sum += v[q];
+  return sum;
+}
+
+// Eight values of x, as loaded, as MMA operands in the pair order (0,4) (1,5) (2,6) (3,7); E4M3 codes become f16
+// (exact).  Volatile: the values are loaded a group ahead, and moved up to their load these would wait for it.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm volatile("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
   return h;
 }
-
-// Eight values of x, as loaded, as MMA operands in the pair order (0,4) (1,5) (2,6) (3,7).
 __device__ __forceinline__ uint4 pair_order(const uint4& v) {
-  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                    __byte_perm(v.y, v.w, 0x7632));
+  return make_uint4(prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632), prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
 }
 __device__ __forceinline__ uint4 pair_order(const uint2& v) {
-  const uint32_t a = __byte_perm(v.x, v.y, 0x5140), c = __byte_perm(v.x, v.y, 0x7362);
+  const uint32_t a = prmt(v.x, v.y, 0x5140), c = prmt(v.x, v.y, 0x7362);
   return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(c), e4m3x2_to_f16x2(c >> 16));
 }
 
-// The launch of a projection kernel: clusters of p.split CTAs along x.
-template <typename Kernel>
-cudaError_t launch_w4(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const W4Params& p) {
+// The launch of a projection kernel: clusters of `split` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_w4(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int split,
+                      const Args&... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.x = split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -99,7 +118,7 @@ cudaError_t launch_w4(Kernel kernel, dim3 grid, int threads, size_t smem, cudaSt
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = launch_overlap() > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // More than a few tokens (csrc/linear_w4_tc.cu).

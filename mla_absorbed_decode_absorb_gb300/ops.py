@@ -97,17 +97,16 @@ def _check(where: str, status: int) -> None:
         raise MLAError(where, status)
 
 
-def _device() -> int:
-    """The current device, on which the kernels run."""
-    if not torch.cuda.is_initialized():
-        torch.cuda.init()
-    return torch._C._cuda_getDevice()
+_device = torch._C._cuda_getDevice  # the current device, on which the kernels run
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
     if stream is None:
         # the raw handle of torch.cuda.current_stream(), without building its Python object
-        return torch._C._cuda_getCurrentRawStream(_device())
+        if device is None:
+            torch.cuda.init()
+            device = _device()
+        return torch._C._cuda_getCurrentRawStream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -266,14 +265,6 @@ def _arg(t, name: str, dtype, shape, device: int) -> int:
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _matrix(t, name: str):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    return t.shape
-
-
 def _new(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -299,7 +290,7 @@ def _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream):
         None if y is None else _arg(y, "y", torch.bfloat16, shape, dev),
         None if y8 is None else _arg(y8, "y8", torch.uint8, shape, dev),
         None if y_scale is None else _arg(y_scale, "y_scale", torch.float32, (T, _groups(D)), dev),
-        T, D, _stream(stream)))
+        T, D, _stream(stream, dev)))
 
 
 def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, stream=None):
@@ -307,9 +298,8 @@ def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, 
 
     x [T, D] may have a row stride (a multiple of 8); with ``residual`` the sum h is written to
     ``residual_out`` (default: in place)."""
-    shape = _matrix(x, "x")
     if y is None:
-        y = _new(shape, torch.bfloat16, x)
+        y = _new(x.shape, torch.bfloat16, x)
     _rms_norm(x, weight, eps, residual, residual_out, y, None, None, stream)
     return y
 
@@ -318,7 +308,7 @@ def mla_rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y8=N
                      stream=None):
     """:func:`mla_rms_norm` with an 8-bit output: (E4M3 codes [T, D] uint8, scales [T, ceil(D/128)] float32),
     what ``mla_linear_w4_fp8`` reads.  With ``y`` the bf16 output is written too."""
-    T, D = shape = _matrix(x, "x")
+    T, D = shape = x.shape
     if y8 is None:
         y8 = _new(shape, torch.uint8, x)
     if y_scale is None:
@@ -329,7 +319,7 @@ def mla_rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y8=N
 
 def mla_quantize_w4(w, w4=None, w_scale=None, stream=None):
     """4-bit weights of ``w [N, K]`` bf16: (half bytes [N, K/2] uint8, scales [N, ceil(K/128)] bf16)."""
-    N, K = shape = _matrix(w, "w")
+    N, K = shape = w.shape
     dev, codes, scales = _device(), (N, K // 2), (N, _groups(K))
     if w4 is None:
         w4 = _new(codes, torch.uint8, w)
@@ -337,45 +327,45 @@ def mla_quantize_w4(w, w4=None, w_scale=None, stream=None):
         w_scale = _new(scales, torch.bfloat16, w)
     _check("mla_quantize_w4", lib.mla_quantize_w4(
         _arg(w, "w", torch.bfloat16, shape, dev), _arg(w4, "w4", torch.uint8, codes, dev),
-        _arg(w_scale, "w_scale", torch.bfloat16, scales, dev), N, K, _stream(stream)))
+        _arg(w_scale, "w_scale", torch.bfloat16, scales, dev), N, K, _stream(stream, dev)))
     return w4, w_scale
 
 
 def mla_dequantize_w4(w4, w_scale, w=None, stream=None):
     """``w [N, K]`` bf16 of 4-bit weights."""
-    N, half = codes = _matrix(w4, "w4")
+    N, half = codes = w4.shape
     K, dev = 2 * half, _device()
     if w is None:
         w = _new((N, K), torch.bfloat16, w4)
     _check("mla_dequantize_w4", lib.mla_dequantize_w4(
         _arg(w4, "w4", torch.uint8, codes, dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev),
-        _arg(w, "w", torch.bfloat16, (N, K), dev), N, K, _stream(stream)))
+        _arg(w, "w", torch.bfloat16, (N, K), dev), N, K, _stream(stream, dev)))
     return w
 
 
 def mla_linear_w4(x, w4, w_scale, y=None, stream=None):
     """``y [T, N] = x [T, K] w^T`` in bf16 with 4-bit weights (fp32 accumulation, no workspace)."""
-    T, K = shape = _matrix(x, "x")
-    N, dev = _matrix(w4, "w4")[0], _device()
+    T, K = shape = x.shape
+    N, dev = w4.shape[0], _device()
     if y is None:
         y = _new((T, N), torch.bfloat16, x)
     _check("mla_linear_w4", lib.mla_linear_w4(
         _arg(x, "x", torch.bfloat16, shape, dev), _arg(w4, "w4", torch.uint8, (N, K // 2), dev),
         _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev), _arg(y, "y", torch.bfloat16, (T, N), dev),
-        T, K, N, _stream(stream)))
+        T, K, N, _stream(stream, dev)))
     return y
 
 
 def mla_linear_w4_fp8(x8, x_scale, w4, w_scale, y=None, stream=None):
     """:func:`mla_linear_w4` of 8-bit activations as :func:`mla_rms_norm_fp8` returns them."""
-    T, K = shape = _matrix(x8, "x8")
-    N, dev, groups = _matrix(w4, "w4")[0], _device(), _groups(K)
+    T, K = shape = x8.shape
+    N, dev, groups = w4.shape[0], _device(), _groups(K)
     if y is None:
         y = _new((T, N), torch.bfloat16, x8)
     _check("mla_linear_w4_fp8", lib.mla_linear_w4_fp8(
         _arg(x8, "x8", torch.uint8, shape, dev), _arg(x_scale, "x_scale", torch.float32, (T, groups), dev),
         _arg(w4, "w4", torch.uint8, (N, K // 2), dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, groups), dev),
-        _arg(y, "y", torch.bfloat16, (T, N), dev), T, K, N, _stream(stream)))
+        _arg(y, "y", torch.bfloat16, (T, N), dev), T, K, N, _stream(stream, dev)))
     return y
 
 
@@ -386,7 +376,7 @@ def mla_read_kv_fp8(cache_fp8, page_table, kv_lens, max_kv_len, rows=None, strea
     c8, scale, kr = cache_fp8
     dev, max_kv_len = _device(), int(max_kv_len)
     B, P = kv_lens.shape[0], c8.shape[0]
-    slots = _matrix(page_table, "page_table")[1]
+    slots = page_table.shape[1]
     shape = (B * ((max_kv_len + 63) // 64), 64, D_ROW)
     if rows is None:
         rows = empty_cache(shape[0], c8.device)
@@ -396,7 +386,7 @@ def mla_read_kv_fp8(cache_fp8, page_table, kv_lens, max_kv_len, rows=None, strea
         _arg(kr, "cache_kr", torch.float16, (P, 64, D_ROPE), dev), P,
         _arg(page_table, "page_table", torch.int32, (B, slots), dev), slots,
         _arg(kv_lens, "kv_lens", torch.int32, (B,), dev), B, max_kv_len,
-        _arg(rows, "rows", torch.bfloat16, shape, dev), _stream(stream)))
+        _arg(rows, "rows", torch.bfloat16, shape, dev), _stream(stream, dev)))
     return rows
 
 
