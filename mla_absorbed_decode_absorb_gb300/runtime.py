@@ -23,6 +23,8 @@ kernel's prologue overlap the previous one.
 With the workload's ``cache_format`` "fp8" the cache is the FP8 latent cache
 (E4M3 codes with one scale per token) and steps 1 and 3 are
 ``mla_append_kv_fp8`` and ``mla_decode_attn_fp8_partial``; the rest is unchanged.
+The non-absorbed path reads bf16 rows: over an FP8 cache ``mla_read_kv_fp8``
+first reads every sequence back into pages of its own.
 
 A step that brings ``PREFILL_MIN_NEW_TOKENS`` (64) or more new tokens per
 sequence takes the non-absorbed path instead, as inference engines switch for
@@ -33,10 +35,12 @@ which give the same per-head output ``out``.
 
 from __future__ import annotations
 
+from dataclasses import dataclass
+
 import torch
 
 from . import ops
-from .workloads import D_LATENT, D_NOPE, D_ROW, N_HEADS, Inputs, empty_cache
+from .workloads import D_LATENT, D_NOPE, D_ROW, N_HEADS, PAGE, Inputs, empty_cache
 
 
 # New tokens per sequence from which a step takes the non-absorbed path (the
@@ -87,8 +91,6 @@ class DecodeSession:
         if path not in ("absorbed", "non_absorbed"):
             raise ValueError(f"unknown path {path!r}")
         self.path = path
-        if self.cache_format == "fp8" and path != "absorbed":
-            raise ValueError("the FP8 latent cache is read by the absorbed path only")
         # append + absorb_q as one launch (both on the caller's stream)
         self.fused_prologue = bool(fused_prologue) and path == "absorbed" and not self.overlap_append
         dev = self.device
@@ -130,6 +132,12 @@ class DecodeSession:
             self.k_nope = torch.empty(kv_shape, dtype=torch.bfloat16, device=dev)
             self.v = torch.empty(kv_shape, dtype=torch.bfloat16, device=dev)
             self.num_splits = 1
+            # the bf16 rows this path reads: the cache itself, or the FP8 cache read back
+            self.kv_rows, self.kv_table = self.cache, self.page_table
+            if self.cache_format == "fp8":
+                pages = (self.max_kv_len + PAGE - 1) // PAGE
+                self.kv_rows = empty_cache(self.B * pages, dev)
+                self.kv_table = torch.arange(self.B * pages, dtype=torch.int32, device=dev).view(self.B, pages)
         if self.overlap_append:
             self.side = torch.cuda.Stream(device=dev)
             self._forked = torch.cuda.Event()
@@ -226,19 +234,25 @@ class DecodeSession:
                                    self.o_latent, self.w_uv, self.out if out is None else out, self.lse,
                                    stream=stream)
 
+    def read_back(self, stream=None):
+        if self.overlap_append:
+            self._main(stream).wait_event(self._appended)  # the cache holds the new tokens
+        ops.mla_read_kv_fp8(self.cache_fp8, self.page_table, self.kv_lens, self.max_kv_len, self.kv_rows, stream=stream)
+
     def decompress(self, stream=None):
         if self.overlap_append:
             self._main(stream).wait_event(self._appended)  # the cache holds the new tokens
-        ops.mla_decompress_kv(self.cache, self.page_table, self.kv_lens, self.max_kv_len, self.w_uk, self.w_uv,
+        ops.mla_decompress_kv(self.kv_rows, self.kv_table, self.kv_lens, self.max_kv_len, self.w_uk, self.w_uv,
                               self.k_nope, self.v, stream=stream)
 
     def prefill_attn(self, stream=None):
-        ops.mla_prefill_attn(self.q_nope, self.q_rope, self.prior_lens, self.rope, self.k_nope, self.v, self.cache,
-                             self.page_table, self.kv_lens, self.out, self.lse, stream=stream)
+        ops.mla_prefill_attn(self.q_nope, self.q_rope, self.prior_lens, self.rope, self.k_nope, self.v, self.kv_rows,
+                             self.kv_table, self.kv_lens, self.out, self.lse, stream=stream)
 
     def stage_names(self) -> list[str]:
         if self.path == "non_absorbed":
-            return ["append", "decompress", "prefill_attn"]
+            read = ["read_back"] if self.cache_format == "fp8" else []
+            return ["append"] + read + ["decompress", "prefill_attn"]
         tail = ["finish"] if self.fused_finish else ["combine", "project_out"]
         head = ["append_absorb"] if self.fused_prologue else ["append", "absorb"]
         return head + ["attend_partial"] + tail
@@ -267,11 +281,22 @@ class DecodeSession:
 
     def launches_per_step(self) -> int:
         if self.path == "non_absorbed":
-            return 3
+            return len(self.stage_names())
         n = 3 if self.fused_prologue else 4
         if self.fused_finish:
             return n
         return n + (1 if self.num_splits > 1 else 0)
+
+
+@dataclass
+class LayerNorms:
+    """The root-mean-square norm weights of one MLA layer (bf16): of the hidden state [d_model] before the
+    projections, of the query's latent c^Q [d_c'] and of the key-value latent c^KV [512]."""
+
+    hidden: torch.Tensor
+    q_latent: torch.Tensor
+    kv_latent: torch.Tensor
+    eps: float = 1e-6
 
 
 class LayerSession:
@@ -297,11 +322,35 @@ class LayerSession:
     (no absorb_q); after the attention the merged latent output O' is rounded to
     bf16 and ``proj_out`` is one linear with W_OV [d_model, 128 * 512] (no W_UV
     step).  The folded weights are 201 MB and 940 MB against 66 MB and 252 MB.
+
+    With ``norms`` (:class:`LayerNorms`) the step begins with ``norm_in``: the hidden
+    state is normed (``mla_rms_norm``), and c^Q and c^KV are normed behind their
+    projections.  With ``residual`` [B, n_q, d_model] besides, ``norm_in`` first adds
+    the hidden state to it, in place (the residual stream).
+
+    ``weights="w4"`` holds the six projections in 4 bits with group scales
+    (``mla_quantize_w4`` once, ``mla_linear_w4`` a step: 0.52 bytes a weight instead of
+    2; not with ``fold``).  ``activations="fp8"`` (with norms and 4-bit weights) lets
+    the norms of the hidden state and of c^Q write 8 bits, which the projections
+    behind them read (``mla_rms_norm_fp8``, ``mla_linear_w4_fp8``).
     """
 
-    def __init__(self, li, device="cuda", split_pages: int | None = None, stream=None, fold: bool = False):
+    def __init__(self, li, device="cuda", split_pages: int | None = None, stream=None, fold: bool = False,
+                 weights: str = "bf16", norms: LayerNorms | None = None, residual: torch.Tensor | None = None,
+                 activations: str = "bf16"):
+        if weights not in ("bf16", "w4"):
+            raise ValueError(f"unknown weight format {weights!r}")
+        if activations not in ("bf16", "fp8"):
+            raise ValueError(f"unknown activation format {activations!r}")
+        if weights == "w4" and fold:
+            raise ValueError("the weight pre-folds are bf16")
+        if activations == "fp8" and (weights != "w4" or norms is None):
+            raise ValueError("8-bit activations come from the norms and go to 4-bit weights")
+        if residual is not None and norms is None:
+            raise ValueError("the residual is added before the norm of the hidden state")
         self.li = li
         self.fold = bool(fold)
+        self.weights, self.activations = weights, activations
         dev = torch.device(device)
         self.device = dev
         self.dec = DecodeSession(li.base, device=dev, split_pages=split_pages, stream=stream)
@@ -313,6 +362,12 @@ class LayerSession:
         self.w_uq, self.w_qr, self.w_o = li.w_uq.to(dev), li.w_qr.to(dev), li.w_o.to(dev)
         self.c_q = torch.empty(self.T, self.w_dq.shape[0], dtype=torch.bfloat16, device=dev)
         self.y = torch.empty(self.T, self.d_model, dtype=torch.bfloat16, device=dev)
+        self.norms = None if norms is None else LayerNorms(norms.hidden.to(dev), norms.q_latent.to(dev),
+                                                           norms.kv_latent.to(dev), float(norms.eps))
+        self.residual = None if residual is None else residual.to(dev).reshape(self.T, self.d_model).contiguous()
+        if self.norms is not None:
+            self.c_kv = torch.empty(self.T, D_LATENT, dtype=torch.bfloat16, device=dev)
+            self._x_normed, self._cq_normed = self._normed(self.x), self._normed(self.c_q)
         # step inputs of the decode session, viewed as [tokens, features]
         self._c_new = d.c_new.view(self.T, -1)
         self._k_new = d.k_new.view(self.T, -1)
@@ -324,6 +379,10 @@ class LayerSession:
         need = max(need, ops.mla_linear_pair_workspace_size(self.T, self.d_model, self.w_dkv.shape[0],
                                                             self.w_kr.shape[0]))
         self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        if weights == "w4":
+            # laid out once; the bf16 weights are not kept
+            for name in ("w_dkv", "w_kr", "w_dq", "w_uq", "w_qr", "w_o"):
+                setattr(self, name, ops.mla_quantize_w4(getattr(self, name), stream=stream))
         # a layer step's input is the hidden state, its result the layer output
         self.step_buffer = self.x
         self.out = self.y
@@ -372,20 +431,57 @@ class LayerSession:
     def download(self, host_out: torch.Tensor, stream=None):
         ops.mla_copy(host_out, self.y, stream)
 
+    def _normed(self, like):
+        """Where a norm's output goes: a bf16 tensor, or (codes, scales) for 8-bit activations."""
+        if self.activations == "bf16":
+            return torch.empty_like(like)
+        return (torch.empty(like.shape, dtype=torch.uint8, device=self.device),
+                torch.empty(like.shape[0], (like.shape[1] + ops.W4_GROUP - 1) // ops.W4_GROUP, dtype=torch.float32,
+                            device=self.device))
+
+    def _norm(self, x, weight, out, stream, residual=None):
+        if isinstance(out, tuple):
+            ops.mla_rms_norm_fp8(x, weight, self.norms.eps, residual, None, *out, stream=stream)
+        else:
+            ops.mla_rms_norm(x, weight, self.norms.eps, residual, y=out, stream=stream)
+
+    def _linear(self, x, w, y, stream):
+        if isinstance(x, tuple):
+            ops.mla_linear_w4_fp8(*x, *w, y, stream=stream)
+        elif self.weights == "w4":
+            ops.mla_linear_w4(x, *w, y, stream=stream)
+        else:
+            ops.mla_linear(x, w, y, self.ws, stream)
+
+    def norm_in(self, stream=None):
+        self._norm(self.x, self.norms.hidden, self._x_normed, stream, self.residual)
+
     def proj_kv(self, stream=None):
-        # W_DKV and W_KR read the same hidden state: one launch
-        ops.mla_linear_pair(self.x, self.w_dkv, self.w_kr, self._c_new, self._k_new, self.ws, stream)
+        x = self.x if self.norms is None else self._x_normed
+        c_kv = self._c_new if self.norms is None else self.c_kv
+        if self.weights == "w4":
+            self._linear(x, self.w_dkv, c_kv, stream)
+            self._linear(x, self.w_kr, self._k_new, stream)
+        else:
+            # W_DKV and W_KR read the same hidden state: one launch
+            ops.mla_linear_pair(x, self.w_dkv, self.w_kr, c_kv, self._k_new, self.ws, stream)
+        if self.norms is not None:
+            ops.mla_rms_norm(self.c_kv, self.norms.kv_latent, self.norms.eps, y=self._c_new, stream=stream)
 
     def proj_q(self, stream=None):
-        ops.mla_linear(self.x, self.w_dq, self.c_q, self.ws, stream)
+        c_q = self.c_q
+        self._linear(self.x if self.norms is None else self._x_normed, self.w_dq, c_q, stream)
+        if self.norms is not None:
+            self._norm(c_q, self.norms.q_latent, self._cq_normed, stream)
+            c_q = self._cq_normed
         if self.fold:
             d = self.dec
-            ops.mla_linear_strided(self.c_q, self.w_qk, d.q_abs, N_HEADS * D_ROW, D_LATENT, D_ROW, self.ws, stream)
-            ops.mla_linear(self.c_q, self.w_qr, self._q_rope, self.ws, stream)
+            ops.mla_linear_strided(c_q, self.w_qk, d.q_abs, N_HEADS * D_ROW, D_LATENT, D_ROW, self.ws, stream)
+            ops.mla_linear(c_q, self.w_qr, self._q_rope, self.ws, stream)
             ops.mla_rope_q(d.q_rope, d.prior_lens, d.rope, d.q_abs, stream=stream)
             return
-        ops.mla_linear(self.c_q, self.w_uq, self._q_nope, self.ws, stream)
-        ops.mla_linear(self.c_q, self.w_qr, self._q_rope, self.ws, stream)
+        self._linear(c_q, self.w_uq, self._q_nope, stream)
+        self._linear(c_q, self.w_qr, self._q_rope, stream)
 
     def to_bf16(self, stream=None):
         ops.mla_f32_to_bf16(self.dec.o_latent, self.o_lat_bf16, stream=stream)
@@ -394,12 +490,17 @@ class LayerSession:
         if self.fold:
             ops.mla_linear(self.o_lat_bf16, self.w_ov, self.y, self.ws, stream)
             return
-        ops.mla_linear(self.dec.out.view(self.T, -1), self.w_o, self.y, self.ws, stream)
+        self._linear(self.dec.out.view(self.T, -1), self.w_o, self.y, stream)
 
     def stage_names(self) -> list[str]:
+        head = ["proj_kv", "proj_q"] if self.norms is None else ["norm_in", "proj_kv", "proj_q"]
         if self.fold:
-            return ["proj_kv", "proj_q", "append", "attend_partial", "combine", "to_bf16", "proj_out"]
-        return ["proj_kv", "proj_q"] + self.dec.stage_names() + ["proj_out"]
+            return head + ["append", "attend_partial", "combine", "to_bf16", "proj_out"]
+        return head + self.dec.stage_names() + ["proj_out"]
+
+    def capture(self, warmup: int = 2) -> "StepGraph":
+        """The layer's step as one CUDA graph.  With ``residual``, the warm-up steps and every replay add to it."""
+        return StepGraph(self, warmup)
 
     def __getattr__(self, name):
         # the decode stages (append, absorb, attend_partial, finish, ...) run on the decode session
@@ -421,7 +522,11 @@ class LayerSession:
             lin = [(self.w_dq, d), (self.w_qk, dq), (self.w_qr, dq), (self.w_ov, self.w_ov.shape[1])]
         else:
             n = self.dec.launches_per_step()
-            lin = [(self.w_dq, d), (self.w_uq, dq), (self.w_qr, dq), (self.w_o, self.w_o.shape[1])]
+            lin = [(self.w_dq, d), (self.w_uq, dq), (self.w_qr, dq), (self.w_o, N_HEADS * D_NOPE)]
+        if self.norms is not None:
+            n += 3
+        if self.weights == "w4":
+            return n + 2 + len(lin)  # one launch each, W_DKV and W_KR among them
         for w, k in lin:
             n += 1 + (1 if ops.mla_linear_workspace_size(self.T, k, w.shape[0]) else 0)
         # W_DKV and W_KR in one launch (plus its split-K sum)
