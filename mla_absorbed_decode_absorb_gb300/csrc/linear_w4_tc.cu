@@ -4,19 +4,18 @@
 //   y[t, n] = sum_g sw[n, g] sx[t, g] sum_{k in g} (u[n, k] - 8) x[t, k]
 //
 // One CTA owns 128 output features (the M side) and a range of K, up to kTn tokens
-// (the N side).  Four producer warps turn a group of 128 columns at a time into
-// the MMA's operands: thread r unpacks the 64 bytes of weight row r into 128 exact
-// bf16 (f16 for 8-bit x) values of TMEM lane r, and the warps place x, in the same
-// pair order (0,4) (1,5) (2,6) (3,7) of each 8 columns, into 128-byte-swizzled
-// shared memory.  A thread issues the group's 8 MMAs (K = 16) into one of two TMEM
-// accumulators, and four epilogue warps read it back and add it, scaled in fp32,
-// to their registers: the accumulator holds one group's exact products only, so no
-// scale is ever rounded into a weight.  Operands and accumulators are
-// double-buffered; weights arrive by TMA, eight groups deep, x through registers
-// one group ahead.
+// (the N side), and takes a group of 128 columns at a time.  Producer warps unpack
+// the weights: thread r turns the 64 bytes of weight row r into 128 exact bf16
+// values of TMEM lane r, or for 8-bit x into 128 E4M3 codes of (u - 8) 2^-9, exact too;
+// x comes by TMA into 128-byte-swizzled shared memory as it is.  A thread issues the
+// group's MMAs (8 of K = 16, or 4 of K = 32 on E4M3) into one of two TMEM accumulators,
+// and the epilogue warps read it back and add it, scaled in fp32, to their
+// registers: the accumulator holds one group's exact products only, so no scale is
+// ever rounded into a weight.
 //
-// Two such CTAs share an SM (256 TMEM columns each).  K is split over a cluster,
-// whose partials meet in distributed shared memory in rank order.
+// Up to 64 tokens two such CTAs share an SM (256 TMEM columns each), beyond one with
+// twice the warps.  K is split over a cluster, whose partials meet in distributed
+// shared memory in rank order.
 #include "sm100.cuh"
 #include "tmap.cuh"
 #include "w4.cuh"
@@ -29,10 +28,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kRows = 128;
-constexpr int kStages = 8;                     // groups of weights in flight or in use
+constexpr int kStages = 4;                     // groups of weights in flight or in use
 constexpr int kSlot = kRows * 64;              // a group of weights
 constexpr int kRing = kStages * kSlot;
-constexpr uint32_t kTmemCols = 256;
+constexpr int kMaxCtas = 304;                  // two on each of 152 SMs: more never run at once
 constexpr uint32_t kTmemA = 0;                 // two operands of 64 columns, then two accumulators
 constexpr uint32_t kTmemD = 128;
 
@@ -41,8 +40,9 @@ __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&d)[8]) { tmem_
 
 struct Bars {
   uint64_t weights[kStages];  // a group of weights has landed (TMA)
-  uint64_t ready[2];    // both operands of a group are in place (one arrival per producer warp)
-  uint64_t free[2];     // ... and have been consumed (commit)
+  uint64_t x[4];              // a group of x has landed (TMA)
+  uint64_t ready[2];    // a group's weights (and x's scales) are in place (one arrival per producer warp)
+  uint64_t free[2];     // ... and have been consumed, and its x (commit)
   uint64_t full[2];     // a group's accumulator is complete (commit)
   uint64_t drained[2];  // ... and has been read (one arrival per epilogue warp)
   uint32_t tmem;
@@ -51,29 +51,33 @@ struct Bars {
 
 template <int kTn, bool kFp8>
 struct TcShape {
-  static constexpr int kPerSm = 2;                             // CTAs of an SM
-  static constexpr int kIssuer = 8;                            // warps 0-3 produce, 4-7 add up, 8 and 9 issue MMAs
+  static constexpr int kPerSm = kTn <= 64 ? 2 : 1;             // CTAs of an SM
+  static constexpr int kSets = kTn <= 64 ? 1 : 2;              // of four producer warps
+  static constexpr int kEpilogue = 4 * kSets;                  // first epilogue warp
+  static constexpr int kEpTok = kTn <= 64 ? kTn : 64;          // tokens of an epilogue thread's registers
+  static constexpr int kEpWarps = 4 * (kTn / kEpTok);
+  static constexpr int kIssuer = kEpilogue + kEpWarps;         // first of the two warps that issue MMAs
+  static constexpr int kDCols = kTn <= 64 ? 64 : 128;          // TMEM columns of an accumulator
+  static constexpr uint32_t kTmemCols = kTn <= 64 ? 256 : 512;
   static constexpr int kThreads = 32 * (kIssuer + 2);
-  static constexpr int kBox = kTn * 128;                       // kTn tokens x 64 columns
-  static constexpr int kB = 2 * kBox;                          // a group of x
+  static constexpr int kBox = kTn * 128;                       // kTn tokens x 64 columns (bf16) or 128 (E4M3)
+  static constexpr int kB = kFp8 ? kBox : 2 * kBox;            // a group of x
+  static constexpr int kXStages = 4;                           // groups of x in flight or in use
   static constexpr int kLd = kRows + 4;                        // floats per token of a partial
   static constexpr int kPart = kTn * kLd * 4;                  // the CTA's partial, over the operands
-  static constexpr int kBody = 2 * kB + kRing > kPart ? 2 * kB + kRing : kPart;
+  static constexpr int kBody = kXStages * kB + kRing > kPart ? kXStages * kB + kRing : kPart;
   static constexpr int kSx = kFp8 ? 4 * kTn * 4 : 0;           // scales of x, four groups
   static constexpr int kSmem = kBody + kSx + 256 + 1024;
   static_assert(sizeof(Bars) <= 256, "barrier block");
 };
 
-template <int kTn, bool kFp8, bool kRagged>
+template <int kTn, bool kFp8>
 __global__ void __launch_bounds__(TcShape<kTn, kFp8>::kThreads, TcShape<kTn, kFp8>::kPerSm)
-linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) {
+linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const W4Params p) {
   using S = TcShape<kTn, kFp8>;
-  using Vec = std::conditional_t<kFp8, uint2, uint4>;  // 8 values of x
-  constexpr int kElem = kFp8 ? 1 : 2;
-  constexpr int kUnits = kTn / 8;  // of 8 values of x per producer thread and group
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ring = smem + 2 * S::kB;
+  uint8_t* ring = smem + S::kXStages * S::kB;
   float* sxs = reinterpret_cast<float*>(smem + S::kBody);  // [4][kTn]
   Bars& bars = *reinterpret_cast<Bars*>(smem + S::kBody + S::kSx);
   float* part = reinterpret_cast<float*>(smem);
@@ -82,22 +86,22 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) 
   const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
   const int n0 = tile * kRows, t0 = blockIdx.z * kTn;
   const int g0 = rank * p.per, ng = max(0, min(p.groups, g0 + p.per) - g0);
-  const int ragged = kRagged ? p.groups - 1 - g0 : -1;  // the group with 64 columns, if any
   volatile int* abort = &bars.abort;
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars.weights[i]), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars.x[i]), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&bars.ready[b]), 4);
       mbar_init(smem_u32(&bars.free[b]), 1);
       mbar_init(smem_u32(&bars.full[b]), 1);
-      mbar_init(smem_u32(&bars.drained[b]), 4);
+      mbar_init(smem_u32(&bars.drained[b]), S::kEpWarps);
     }
     bars.abort = 0;
     fence_mbar_init();
   }
   if (warp == S::kIssuer) {
-    tmem_alloc(smem_u32(&bars.tmem), kTmemCols);
+    tmem_alloc(smem_u32(&bars.tmem), S::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -107,34 +111,20 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) 
   if (!p.early || warp < S::kIssuer) grid_dep_wait();  // the issuers fetch weights
   grid_dep_launch();
 
-  if (warp < 4) {
+  if (warp < S::kEpilogue) {
     // -------------------------------------------------------------- producers
     // Rows past N and columns past K are zeros, tokens past T read as the last one (not stored).
-    const uint8_t* wrow = ring + tid * 64;
-    const int perm = tid >> 1 & 3;  // 64-byte swizzle: 16-byte unit q of row r lies at q ^ (r / 2 % 4)
-    // this thread's units of x: 8 columns of tokens xt, xt + 8, ..
-    const int k = tid & 15;
-    const uint32_t xt = tid >> 4;
-    const uint8_t* xp = static_cast<const uint8_t*>(p.x) +
-                        (static_cast<int64_t>(t0) * p.K + static_cast<int64_t>(g0) * kW4Group + k * 8) * kElem;
-    const uint32_t xput = (k >> 3) * S::kBox + sw128(xt * 128 + (k & 7) * 16);
-    const uint32_t x_ld = static_cast<uint32_t>(p.K) * kElem;  // T K is at most 2^30: 32-bit offsets
-    const uint32_t last = p.T - 1 - t0;
-    Vec xv[kUnits];
-    float sx = 0.f;
-    auto load_x = [&](int i) {
-      if (i >= ng) return;
-      const uint8_t* at = xp + static_cast<int64_t>(i) * (kW4Group * kElem);
-#pragma unroll
-      for (int q = 0; q < kUnits; ++q)
-        xv[q] = kRagged && i == ragged && k >= 8 ? Vec{} : *reinterpret_cast<const Vec*>(at + min(xt + 8 * q, last) * x_ld);
-      if (kFp8 && tid < kTn)
-        sx = p.sx[static_cast<int64_t>(min(t0 + tid, p.T - 1)) * p.groups + g0 + i];
+    const int r = tid & 127, set = tid >> 7;  // a set takes every kSets-th group
+    const uint8_t* wrow = ring + r * 64;
+    const int perm = r >> 1 & 3;  // 64-byte swizzle: 16-byte unit q of row r lies at q ^ (r / 2 % 4)
+    float sx = 0.f;  // the scale of token r's next group
+    auto load_sx = [&](int i) {
+      if (i < ng && r < kTn) sx = p.sx[static_cast<int64_t>(min(t0 + r, p.T - 1)) * p.groups + g0 + i];
     };
-    load_x(0);
+    if (kFp8) load_sx(set);
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     bool ok = true;
-    for (int i = 0; i < ng; ++i) {
+    for (int i = set; i < ng; i += S::kSets) {
       const int b = i & 1;
       ok = mbar_wait(smem_u32(&bars.weights[i % kStages]), (i / kStages) & 1, p.status, abort);
       uint32_t w[16];
@@ -146,29 +136,44 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) 
         w[4 * q + 2] = v.z;
         w[4 * q + 3] = v.w;
       }
+      // The first kAhead parts are unpacked before the operand is free, beside the MMAs that hold it (256 tokens,
+      // 16384 -> 7168: 86 us, against 99 with none; up to 64 tokens the other CTA of the SM fills that time, and the
+      // registers it takes cost more).
+      constexpr int kQuarters = kFp8 ? 2 : 4;  // of 16 TMEM columns
+      uint32_t a[kQuarters][16];
+      auto unpack = [&](int h) {
+#pragma unroll
+        for (int q = 0; q < 16 / kQuarters; ++q) {
+          if (kFp8) {
+            uint32_t c[2];
+            w4_e4m3(w[8 * h + q], c);
+            a[h][2 * q] = c[0];
+            a[h][2 * q + 1] = c[1];
+          } else {
+            uint32_t c[4];
+            w4_pairs_natural(w[4 * h + q], c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[h][4 * q + e] = c[e];
+          }
+        }
+      };
+      constexpr int kAhead = kTn < 128 ? 0 : kQuarters;
+#pragma unroll
+      for (int h = 0; h < kAhead; ++h) unpack(h);
       if (i >= 2) ok = ok && mbar_wait(smem_u32(&bars.free[b]), ((i >> 1) & 1) ^ 1, p.status, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      if (kFp8) {
+        if (r < kTn) sxs[(i & 3) * kTn + r] = sx;
+        load_sx(i + S::kSets);
+      }
 #pragma unroll
-      for (int q = 0; q < kUnits; ++q) *reinterpret_cast<uint4*>(smem + b * S::kB + xput + q * 1024) = pair_order(xv[q]);
-      if (kFp8 && tid < kTn) sxs[(i & 3) * kTn + tid] = sx;
-      load_x(i + 1);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t a[16];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pr[4];
-          if (kFp8) w4_pairs_f16(w[4 * h + q], pr);
-          else w4_pairs(w[4 * h + q], pr);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[4 * q + e] = pr[e];
-        }
-        tmem_st16(tmem + lane_off + kTmemA + 64 * b + 16 * h, a);
+      for (int h = 0; h < kQuarters; ++h) {
+        if (h >= kAhead) unpack(h);
+        tmem_st16(tmem + lane_off + kTmemA + 64 * b + 16 * h, a[h]);
       }
       tmem_wait_st();
       tc_fence_before();
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.ready[b]));
     }
@@ -178,46 +183,68 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) 
     // two warps issue: one the groups of each buffer, which share nothing.
     if (lane == 0) {
       const int b = warp - S::kIssuer;
-      // the weights of this buffer's groups: a slot is free again once its operands are ready
+      // the weights of this buffer's groups: a slot is free again once the producers are ready with it
       auto fetch = [&](int i) {
         if (i >= ng) return;
         const uint32_t bar = smem_u32(&bars.weights[i % kStages]);
         mbar_arrive_expect_tx(bar, kSlot);
         tma_load_2d(smem_u32(ring + (i % kStages) * kSlot), &tm_w, (g0 + i) * 64, n0, bar);
       };
+      // ... and their x: free again once its MMAs have completed
+      auto fetch_x = [&](int i) {
+        if (i >= ng) return;
+        const uint32_t bar = smem_u32(&bars.x[i & 3]), at = smem_u32(smem + (i & 3) * S::kB);
+        mbar_arrive_expect_tx(bar, S::kB);
+        tma_load_2d(at, &tm_x, (g0 + i) * kW4Group, t0, bar);
+        if (!kFp8) tma_load_2d(at + S::kBox, &tm_x, (g0 + i) * kW4Group + 64, t0, bar);
+      };
       int i = b;
       for (; i < kStages; i += 2) fetch(i);
+      if (p.early) grid_dep_wait();
+      fetch_x(b);
+      fetch_x(b + 2);
       const uint32_t idesc = kFp8 ? idesc_f16(128, kTn, 0, 0) : idesc_bf16(128, kTn, 0, 0);
-      int fetched = i;  // first group of this buffer not fetched yet
+      int fetched = i, fetched_x = b + 4;  // first groups of this buffer not fetched yet
       for (i = b; i < ng; i += 2) {
+        if (i >= 2) {
+          if (!mbar_wait(smem_u32(&bars.free[b]), ((i >> 1) & 1) ^ 1, p.status, abort)) break;
+          fetch_x(fetched_x);
+          fetched_x += 2;
+        }
         if (!mbar_wait(smem_u32(&bars.ready[b]), (i >> 1) & 1, p.status, abort)) break;
         fetch(fetched);
         fetched += 2;
+        if (!mbar_wait(smem_u32(&bars.x[i & 3]), (i >> 2) & 1, p.status, abort)) break;
         if (i >= 2 && !mbar_wait(smem_u32(&bars.drained[b]), ((i >> 1) & 1) ^ 1, p.status, abort)) break;
         tc_fence_after();
-        const uint32_t b0 = smem_u32(smem + b * S::kB);
+        const uint32_t b0 = smem_u32(smem + (i & 3) * S::kB);
+        const uint32_t d = tmem + kTmemD + S::kDCols * b, a0 = tmem + kTmemA + 64 * b;
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          mma_ts(tmem + kTmemD + 64 * b, tmem + kTmemA + 64 * b + 8 * q,
-                 smem_desc(b0 + (q >> 2) * S::kBox + (q & 3) * 32, 16, 1024, kSw128), idesc, q ? 1u : 0u);
+        for (int q = 0; q < (kFp8 ? 4 : 8); ++q) {
+          const uint64_t bd = smem_desc(b0 + (q >> 2) * S::kBox + (q & 3) * 32, 16, 1024, kSw128);
+          if (kFp8) mma_ts_f8(d, a0 + 8 * q, bd, idesc, q ? 1u : 0u);
+          else mma_ts(d, a0 + 8 * q, bd, idesc, q ? 1u : 0u);
+        }
         mma_commit(smem_u32(&bars.free[b]));
         mma_commit(smem_u32(&bars.full[b]));
       }
       if (i < ng) {
         // given up: wait for the MMAs and the copies still in flight
         if (i >= 2) mbar_wait(smem_u32(&bars.free[b]), ((i >> 1) & 1) ^ 1, p.status);
-        for (; i < min(ng, fetched); i += 2)
-          mbar_wait(smem_u32(&bars.weights[i % kStages]), (i / kStages) & 1, p.status);
+        for (int j = i; j < min(ng, fetched); j += 2)
+          mbar_wait(smem_u32(&bars.weights[j % kStages]), (j / kStages) & 1, p.status);
+        for (int j = i; j < min(ng, fetched_x); j += 2)
+          mbar_wait(smem_u32(&bars.x[j & 3]), (j >> 2) & 1, p.status);
       }
     }
     __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
-    // TMEM lane = row n0 + 32 (warp % 4) + lane, column = token
-    const int r = (warp & 3) * 32 + lane;
-    float acc[kTn];
+    // TMEM lane = row n0 + 32 (warp % 4) + lane, column = token; a second four warps take the upper 64 tokens
+    const int r = (warp & 3) * 32 + lane, c0 = (warp - S::kEpilogue) / 4 * S::kEpTok;
+    float acc[S::kEpTok];
 #pragma unroll
-    for (int t = 0; t < kTn; ++t) acc[t] = 0.f;
+    for (int t = 0; t < S::kEpTok; ++t) acc[t] = 0.f;
     constexpr int kLoad = kTn < 64 ? 16 : 8;  // columns at a time: 64 sums leave few registers
     const uint16_t* sw = p.sw + static_cast<int64_t>(min(n0 + r, p.N - 1)) * p.groups + g0;
     uint16_t next[4];  // a thread's scales are two bytes of a row of its own: four groups ahead
@@ -226,29 +253,24 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) 
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     bool ok = true;
     for (int i0 = 0; i0 < ng && ok; i0 += 4) {
-      uint16_t cur[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        cur[q] = next[q];
-        next[q] = i0 + 4 + q < ng ? sw[i0 + 4 + q] : uint16_t(0);
-      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = i0 + q, b = q & 1;
         if (i >= ng) break;
+        const float s = bf16_bits_to_f32(next[q]) * (kFp8 ? 512.f : 1.f);  // E4M3 weights carry 2^-9
+        next[q] = i + 4 < ng ? sw[i + 4] : uint16_t(0);
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.full[b]), (i >> 1) & 1, p.status, abort));
         if (!ok) break;
         tc_fence_after();
-        const float s = bf16_bits_to_f32(cur[q]);
 #pragma unroll
-        for (int c = 0; c < kTn; c += kLoad) {
+        for (int c = 0; c < S::kEpTok; c += kLoad) {
           uint32_t d[kLoad];
-          tmem_load(tmem + lane_off + kTmemD + 64 * b + c, d);
+          tmem_load(tmem + lane_off + kTmemD + S::kDCols * b + c0 + c, d);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < kLoad; ++e) {
             const float v = __uint_as_float(d[e]);
-            acc[c + e] = fmaf(kFp8 ? v * sxs[q * kTn + c + e] : v, s, acc[c + e]);
+            acc[c + e] = fmaf(kFp8 ? v * sxs[q * kTn + c0 + c + e] : v, s, acc[c + e]);
           }
         }
         tc_fence_before();
@@ -258,13 +280,13 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) 
     }
     // every MMA has completed: the operands and the ring are free for the partial
 #pragma unroll
-    for (int t = 0; t < kTn; ++t) part[t * S::kLd + r] = acc[t];
+    for (int t = 0; t < S::kEpTok; ++t) part[(c0 + t) * S::kLd + r] = acc[t];
   }
   tc_fence_before();
   if (p.split > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
-  if (warp == S::kIssuer) tmem_dealloc(tmem, kTmemCols);
+  if (warp == S::kIssuer) tmem_dealloc(tmem, S::kTmemCols);
 
   // the cluster's threads share the (token, row) sums, row fastest, each in rank order
   const int toks = min(kTn, p.T - t0);
@@ -278,40 +300,56 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const W4Params p) 
   if (p.split > 1) cluster_sync();  // peers may still be reading this CTA's partial
 }
 
-template <int kTn, bool kFp8, bool kRagged>
-cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
+template <int kTn, bool kFp8>
+cudaError_t launch_tn(W4Params p, cudaStream_t stream) {
   using S = TcShape<kTn, kFp8>;
   static bool configured[kMaxDevicesLocal] = {};  // the attribute is per device
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
-  auto kernel = linear_w4_tc_kernel<kTn, kFp8, kRagged>;
+  auto kernel = linear_w4_tc_kernel<kTn, kFp8>;
   if (!configured[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  const int tiles = (p.N + kRows - 1) / kRows, slices = (p.T + kTn - 1) / kTn;
+  // K over the largest cluster whose CTAs still fit the GPU at once (a second, partial wave costs more: 256 tokens,
+  // 7168 -> 1536 in 24 tiles: 14.0 us in clusters of 5, 24.1 in clusters of 6, which do not all fit) and that leaves a
+  // CTA two groups, or seven where CTAs share an SM (32 tokens, 1536 -> 16384: 10.4 us undivided, 11.7 halved)
+  const int64_t tiles = (p.N + kRows - 1) / kRows, slices = (p.T + kTn - 1) / kTn;
+  static int fit[kMaxDevicesLocal][kW4MaxSplit + 1] = {};  // clusters resident at once, 0: not asked yet
   p.split = 1;
-  for (int s = 2; s <= kW4MaxSplit && tiles * slices * s <= 152 * S::kPerSm && p.groups >= 2 * s; ++s) p.split = s;
+  for (int s = kW4MaxSplit; s > 1; --s) {
+    const int64_t ctas = tiles * slices * s;
+    if (ctas > kMaxCtas || p.groups < (ctas <= kMaxCtas / 2 ? 2 : 7) * s) continue;
+    int n = fit[dev][s];
+    if (n == 0) {
+      const cudaError_t e = w4_clusters(kernel, S::kThreads, S::kSmem, s, &n);
+      if (e != cudaSuccess) return e;
+      n *= S::kPerSm;  // the query counts one CTA an SM here, measured are two (56 clusters of 5: one wave)
+      fit[dev][s] = n;
+    }
+    if (tiles * slices <= n) {
+      p.split = s;
+      break;
+    }
+  }
   p.per = (p.groups + p.split - 1) / p.split;
   p.early = launch_overlap() >= 2;
-  CUtensorMap tm_w;
+  CUtensorMap tm_w, tm_x;
   if (!make_tmap_u8_2d(&tm_w, p.w4, p.N, p.K / 2, p.K / 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  return launch_w4(kernel, dim3(tiles * p.split, 1, slices), S::kThreads, S::kSmem, stream, p.split, tm_w, p);
-}
-
-template <int kTn, bool kFp8>
-cudaError_t launch_tn(const W4Params& p, cudaStream_t stream) {
-  return p.K % kW4Group != 0 ? launch_shape<kTn, kFp8, true>(p, stream) : launch_shape<kTn, kFp8, false>(p, stream);
+  const bool ok = kFp8 ? make_tmap_u8_2d(&tm_x, p.x, p.T, p.K, p.K, kW4Group, kTn, CU_TENSOR_MAP_SWIZZLE_128B)
+                       : make_tmap_bf16_2d(&tm_x, p.x, p.T, p.K, p.K, 64, kTn, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return cudaErrorInvalidValue;
+  return launch_w4(kernel, dim3(static_cast<unsigned>(tiles) * p.split, 1, static_cast<unsigned>(slices)), S::kThreads, S::kSmem, stream, p.split, tm_w, tm_x, p);
 }
 
 template <bool kFp8>
 cudaError_t launch_any(const W4Params& p, cudaStream_t stream) {
   if (p.T <= 16) return launch_tn<16, kFp8>(p, stream);
-  const int slices = (p.T + 63) / 64;
-  if (p.T <= 48 * slices) return launch_tn<48, kFp8>(p, stream);
-  return launch_tn<64, kFp8>(p, stream);
+  if (p.T <= 48) return launch_tn<48, kFp8>(p, stream);
+  if (p.T <= 64) return launch_tn<64, kFp8>(p, stream);
+  return launch_tn<128, kFp8>(p, stream);
 }
 
 }  // namespace

@@ -34,7 +34,30 @@ __device__ __forceinline__ void w4_pairs(uint32_t v, uint32_t (&p)[4]) {
 }
 
 
-// The same pairs in f16: 0x6400 is 1024, whose unit in the last place is 1, so a half byte
+// The eight half bytes in their own order, as pairs (u_{2i} - 8, u_{2i+1} - 8): two instructions more.
+__device__ __forceinline__ void w4_pairs_natural(uint32_t v, uint32_t (&p)[4]) {
+  const uint32_t even = v & 0x0f0f0f0fu, odd = (v >> 4) & 0x0f0f0f0fu;
+  const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);  // u_0 .. u_3, u_4 .. u_7
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t biased = __byte_perm(i < 2 ? lo : hi, 0x43434343u, i & 1 ? 0x4342 : 0x4140);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(biased), "r"(0x43084308u));
+  }
+}
+
+// The eight half bytes in their own order as E4M3 codes of (u - 8) 2^-9: E4M3's subnormals and its first binade have
+// one step, 2^-9, so the code of a magnitude m <= 8 is m itself, and the sign is bit 7.
+__device__ __forceinline__ void w4_e4m3(uint32_t v, uint32_t (&c)[2]) {
+  const uint32_t even = v & 0x0f0f0f0fu, odd = (v >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = __byte_perm(even, odd, i ? 0x7362 : 0x5140);
+    const uint32_t neg = ~(u >> 3) & 0x01010101u;  // 1 in the bytes with u < 8
+    c[i] = ((u & 0x07070707u) ^ (neg * 7u)) + neg * 0x81u;  // u < 8: (7 - u) + 1, sign set; else u - 8
+  }
+}
+
+// The pairs of w4_pairs in f16: 0x6400 is 1024, whose unit in the last place is 1, so a half byte
 // in the low bits adds u and one four bits up adds 16 u; both ways back are exact.
 __device__ __forceinline__ void w4_pairs_f16(uint32_t v, uint32_t (&p)[4]) {
 #pragma unroll
@@ -102,23 +125,38 @@ __device__ __forceinline__ uint4 pair_order(const uint2& v) {
 }
 
 // The launch of a projection kernel: clusters of `split` CTAs along x.
+struct W4Launch {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  W4Launch(dim3 grid, int threads, size_t smem, cudaStream_t stream, int split) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = launch_overlap() > 0 ? 2 : 1;
+  }
+};
 template <typename... KArgs, typename... Args>
 cudaError_t launch_w4(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int split,
                       const Args&... args) {
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = launch_overlap() > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  W4Launch l(grid, threads, smem, stream, split);
+  return cudaLaunchKernelEx(&l.cfg, kernel, args...);
+}
+// Clusters of `split` CTAs that are resident on the current device at once (at least 1).
+template <typename... KArgs>
+cudaError_t w4_clusters(void (*kernel)(KArgs...), int threads, size_t smem, int split, int* n) {
+  W4Launch l(dim3(split), threads, smem, nullptr, split);
+  l.cfg.numAttrs = 1;
+  *n = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kernel, &l.cfg);
+  if (*n < 1) *n = 1;
+  return e;
 }
 
 // More than a few tokens (csrc/linear_w4_tc.cu).

@@ -224,12 +224,61 @@ def test_linear_parity(T, K, N, fp8):
     ok()
 
 
+# Sizes of over 36 M weights times passes of 8 tokens: the tensor-core kernel, its tiles of 16, 48, 64 and 128 tokens
+# each full and ragged, K of one group, half a group and not a multiple of 128, odd widths, K whole and divided.
+@pytest.mark.parametrize("T,K,N", [
+    (9, 1088, 16601), (16, 192, 94000), (16, 7168, 2561), (17, 64, 188001), (33, 1536, 4703), (48, 128, 47000),
+    (49, 320, 16100), (57, 2112, 2200), (64, 1536, 3001), (65, 64, 62600), (100, 1088, 2600), (128, 128, 17600),
+    (129, 576, 3700), (200, 1600, 901), (256, 64, 17700), (256, 16384, 130)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_linear_parity_large(T, K, N, fp8):
+    assert N * K * -(-T // 8) > 36_000_000
+    args = linear_inputs(T, K, N, fp8, T * 131 + K + N)
+    ref, tol = linear_ref(*args)
+    y = run_linear(*args)
+    within(f64(y), ref, tol)
+    again = run_linear(*args)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    ok()
+
+
+@pytest.mark.parametrize("T,N", [(8, 500), (16, 150000), (48, 50000), (64, 36000), (256, 9300)])
+def test_linear_keeps_what_cancels(T, N):
+    """Pairs of columns with one x (2 .. 30) and weights c and -c, and one column of the smallest E4M3 value 2^-9,
+    which is what remains.  A partial sum is a multiple of 2^-9 below 64 * 7 * 30 < 2^14: 23 bits, so nothing is
+    rounded but y, in whatever order the sums are formed."""
+    rng = np.random.default_rng(T)
+    K = 128
+    c = rng.integers(1, 8, (N, K // 2))
+    u = np.empty((N, K), np.int64)
+    u[:, 0::2], u[:, 1::2] = 8 + c, 8 - c
+    codes = rng.integers(0x40, 0x60, (T, K // 2)).astype(np.uint8)  # 2 .. 30
+    x = np.repeat(codes, 2, axis=1)
+    x[:, 0], x[:, 1], u[:, 1] = 1, 1, 8
+    perm = rng.permutation(K)
+    u, x = np.ascontiguousarray(u[:, perm]), np.ascontiguousarray(x[:, perm])
+    w4, scale = torch.tensor(F.pack_w4(u)), torch.ones(N, 1, dtype=torch.bfloat16)
+    xf = O.e4m3_decode(x)
+    ref = F.bf16_round(np.broadcast_to(2.0 ** -9 * c[:, 0], (T, N)))
+    y8 = run_linear(torch.tensor(x), torch.ones(T, 1), w4, scale)
+    assert np.array_equal(f64(y8), ref)
+    y = run_linear(torch.tensor(xf).to(torch.bfloat16), None, w4, scale)
+    assert np.array_equal(f64(y), ref)
+    ok()
+
+
 @pytest.mark.parametrize("T", [1, 5, 32, 48, 256])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_linear_of_extreme_codes(T, fp8):
     """Every weight -8, then every weight 7 (the ends of the range), then 0; the sums are exact integers times
     the scales, and a row of scale 0 gives 0."""
     N, K = 70, 320
+    check_extreme_codes(T, N, K, fp8)
+    if T > 5:
+        check_extreme_codes(T, 36_000_000 // (K * -(-T // 8)) + 71, K, fp8)  # ... and the tensor-core kernel
+
+
+def check_extreme_codes(T, N, K, fp8):
     x, sx, w4, scale = linear_inputs(T, K, N, fp8, 3)
     scale[5] = 0
     for byte, v in ((0x00, -8), (0xff, 7), (0x88, 0)):
@@ -241,11 +290,12 @@ def test_linear_of_extreme_codes(T, fp8):
     ok()
 
 
-@pytest.mark.parametrize("T", [2, 9, 40, 130])
+@pytest.mark.parametrize("T,N", [(2, 100), (9, 100), (9, 32000), (40, 100), (40, 12600), (57, 8000), (130, 100),
+                                 (130, 3700)])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_linear_keeps_a_bad_token_to_itself(T, fp8):
+def test_linear_keeps_a_bad_token_to_itself(T, N, fp8):
     """A NaN in one token's input (its code 0x7F) makes that token's outputs NaN and leaves the others'."""
-    x, sx, w4, scale = linear_inputs(T, 576, 100, fp8, 11)
+    x, sx, w4, scale = linear_inputs(T, 576, N, fp8, 11)
     good = run_linear(x, sx, w4, scale)
     x[1, 570] = 0x7f if fp8 else float("nan")
     y = run_linear(x, sx, w4, scale)
@@ -255,11 +305,11 @@ def test_linear_keeps_a_bad_token_to_itself(T, fp8):
     ok()
 
 
-@pytest.mark.parametrize("T", [1, 20, 70])
-def test_linear_writes_its_rows_only(T):
+@pytest.mark.parametrize("T,N", [(1, 37), (20, 37), (70, 37), (10, 70001), (20, 47001), (60, 17601), (70, 15701)])
+def test_linear_writes_its_rows_only(T, N):
     """y in the middle of a larger buffer, at an odd row width (no alignment beyond an element's)."""
-    x, sx, w4, scale = linear_inputs(T, 256, 37, False, 21)
-    buf = torch.full((T + 2, 37), 77.0, dtype=torch.bfloat16, device="cuda")
+    x, sx, w4, scale = linear_inputs(T, 256, N, False, 21)
+    buf = torch.full((T + 2, N), 77.0, dtype=torch.bfloat16, device="cuda")
     run_linear(x, sx, w4, scale, y=buf[1:T + 1])
     ref, tol = linear_ref(x, sx, w4, scale)
     within(f64(buf[1:T + 1]), ref, tol)
