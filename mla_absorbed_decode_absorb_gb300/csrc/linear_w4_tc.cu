@@ -56,6 +56,9 @@ struct TcShape {
   static constexpr int kEpilogue = 4 * kSets;                  // first epilogue warp
   static constexpr int kEpTok = kTn <= 64 ? kTn : 64;          // tokens of an epilogue thread's registers
   static constexpr int kEpWarps = 4 * (kTn / kEpTok);
+  // Packed fp32 sums where the registers allow pairs (256 tokens, 16384 -> 7168: 80 us against 84; 32 tokens 25.0 against
+  // 26.2); 64 sums and x's scales in pairs spill (256 tokens in 8 bits: 140 us against 95).
+  static constexpr bool kPacked = kEpTok < 64 || (kTn == 128 && !kFp8);
   static constexpr int kIssuer = kEpilogue + kEpWarps;         // first of the two warps that issue MMAs
   static constexpr int kDCols = kTn <= 64 ? 64 : 128;          // TMEM columns of an accumulator
   static constexpr uint32_t kTmemCols = kTn <= 64 ? 256 : 512;
@@ -137,7 +140,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         w[4 * q + 3] = v.w;
       }
       // The first kAhead parts are unpacked before the operand is free, beside the MMAs that hold it (256 tokens,
-      // 16384 -> 7168: 86 us, against 99 with none; up to 64 tokens the other CTA of the SM fills that time, and the
+      // 16384 -> 7168: 86 us, against 99 with none, before the sums were packed; up to 64 tokens the other CTA of the SM fills that time, and the
       // registers it takes cost more).
       constexpr int kQuarters = kFp8 ? 2 : 4;  // of 16 TMEM columns
       uint32_t a[kQuarters][16];
@@ -268,9 +271,20 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
           tmem_load(tmem + lane_off + kTmemD + S::kDCols * b + c0 + c, d);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < kLoad; ++e) {
-            const float v = __uint_as_float(d[e]);
-            acc[c + e] = fmaf(kFp8 ? v * sxs[q * kTn + c0 + c + e] : v, s, acc[c + e]);
+          for (int e = 0; e < kLoad; e += 2) {
+            const float v0 = __uint_as_float(d[e]), v1 = __uint_as_float(d[e + 1]);
+            const float* sx = sxs + q * kTn + c0 + c + e;
+            float* to = acc + c + e;
+            if (S::kPacked) {
+              uint64_t v = f32x2(v0, v1);
+              if (kFp8) v = mul_f32x2(v, *reinterpret_cast<const uint64_t*>(sx));
+              const float2 sum = f32x2_split(fma_f32x2(v, f32x2(s, s), f32x2(to[0], to[1])));
+              to[0] = sum.x;
+              to[1] = sum.y;
+            } else {
+              to[0] = fmaf(kFp8 ? v0 * sx[0] : v0, s, to[0]);
+              to[1] = fmaf(kFp8 ? v1 * sx[1] : v1, s, to[1]);
+            }
           }
         }
         tc_fence_before();
