@@ -497,12 +497,16 @@ mla_status mla_rms_norm(const mla_bf16* x, int64_t x_ld, const mla_bf16* residua
  *   with such weights.  x [T, K] bf16, y [T, N] bf16 out, 1 <= T <= MLA_LINEAR_MAX_T.
  * mla_linear_w4_fp8 -- the same with 8-bit x as mla_rms_norm writes it: x8 [T, K]
  *   E4M3 codes, x_scale [T, ceil(K / 128)] float32, x = E4M3(x8) * x_scale.
+ * mla_linear_w4_pair, mla_linear_w4_fp8_pair -- two projections of the same x in one
+ *   launch, y0 = x W0^T [T, N0] and y1 = x W1^T [T, N1], as mla_linear_pair: a launch
+ *   fewer where few tokens leave the projections latency-bound (K may be split
+ *   differently from two calls, which only reorders the float32 sums).
  * The products u - 8 times x are exact and summed in float32, the scales are
  * applied to each group's sum in float32, and y is rounded once.  K is split
  * over the CTAs of a cluster, whose partials are added in a fixed order on
  * chip: no workspace, and a result that does not depend on timing.
  * N >= 1, K >= 64 a multiple of 64; the projections take K <= MLA_W4_MAX_K
- * (MLA_ERR_UNSUPPORTED beyond); y must not overlap an input.
+ * (MLA_ERR_UNSUPPORTED beyond); an output must not overlap an input or the other.
  */
 #define MLA_W4_GROUP 128
 #define MLA_W4_MAX_K 4194304
@@ -513,6 +517,12 @@ mla_status mla_linear_w4(const mla_bf16* x, const uint8_t* w4, const mla_bf16* w
                          int T, int K, int N, cudaStream_t stream);
 mla_status mla_linear_w4_fp8(const uint8_t* x8, const float* x_scale, const uint8_t* w4, const mla_bf16* w_scale,
                              mla_bf16* y, int T, int K, int N, cudaStream_t stream);
+mla_status mla_linear_w4_pair(const mla_bf16* x, int T, int K, const uint8_t* w4_0, const mla_bf16* w_scale_0, int N0,
+                              mla_bf16* y0, const uint8_t* w4_1, const mla_bf16* w_scale_1, int N1, mla_bf16* y1,
+                              cudaStream_t stream);
+mla_status mla_linear_w4_fp8_pair(const uint8_t* x8, const float* x_scale, int T, int K, const uint8_t* w4_0,
+                                  const mla_bf16* w_scale_0, int N0, mla_bf16* y0, const uint8_t* w4_1,
+                                  const mla_bf16* w_scale_1, int N1, mla_bf16* y1, cudaStream_t stream);
 
 /*
  * mla_read_kv_fp8 -- the FP8 latent cache read back into bf16 rows, so that the

@@ -11,7 +11,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "internal.cuh"
+#include "w4.cuh"
 
 // Per-device fault word written by the kernels (first code wins).
 __device__ int g_mla_device_status;
@@ -74,19 +74,39 @@ mla_status w4_check(const uint8_t* w4, const mla_bf16* w_scale, int N, int K) {
   return MLA_OK;
 }
 
-mla_status linear_w4_check(const void* x, int x_elem, const float* x_scale, const uint8_t* w4,
-                           const mla_bf16* w_scale, const mla_bf16* y, int T, int K, int N) {
+// The projections' checks and launch: x in bf16 (x_scale nullptr, x_elem 2) or E4M3, outputs out[0 .. n).
+mla_status linear_w4(const void* x, int x_elem, const float* x_scale, const W4Out* out, int n, int T, int K,
+                     cudaStream_t stream) {
   if (T < 1 || T > MLA_LINEAR_MAX_T) return MLA_ERR_INVALID_ARG;
-  const mla_status s = w4_check(w4, w_scale, N, K);
-  if (s != MLA_OK) return s;
-  if (K > MLA_W4_MAX_K) return MLA_ERR_UNSUPPORTED;  // x is indexed in 32 bits
-  if (!x || !y || !aligned16(x) || (reinterpret_cast<uintptr_t>(y) & 1u) != 0) return MLA_ERR_INVALID_ARG;
-  const Range out{y, static_cast<size_t>(T) * N * 2};
-  const size_t groups = (static_cast<size_t>(K) + MLA_W4_GROUP - 1) / MLA_W4_GROUP;
-  if (overlap(out, {x, static_cast<size_t>(T) * K * x_elem}) || overlap(out, {x_scale, T * groups * sizeof(float)}) ||
-      overlap(out, w4_range(w4, N, K)) || overlap(out, w4_scale_range(w_scale, N, K)))
-    return MLA_ERR_INVALID_ARG;
-  return MLA_OK;
+  if (!x || !aligned16(x) || !aligned16(x_scale)) return MLA_ERR_INVALID_ARG;
+  const size_t groups = (static_cast<size_t>(K > 0 ? K : 0) + MLA_W4_GROUP - 1) / MLA_W4_GROUP;
+  const Range xr{x, static_cast<size_t>(T) * (K > 0 ? K : 0) * x_elem}, sr{x_scale, T * groups * sizeof(float)};
+  for (int i = 0; i < n; ++i) {
+    const W4Out& o = out[i];
+    const mla_status s = w4_check(o.w4, o.sw, o.N, K);
+    if (s != MLA_OK) return s;
+    if (!o.y || (reinterpret_cast<uintptr_t>(o.y) & 1u) != 0) return MLA_ERR_INVALID_ARG;
+    const Range y{o.y, static_cast<size_t>(T) * o.N * 2};
+    if (overlap(y, xr) || overlap(y, sr)) return MLA_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j) {
+      const Range other{out[j].y, static_cast<size_t>(T) * (out[j].N > 0 ? out[j].N : 0) * 2};
+      if (overlap(y, w4_range(out[j].w4, out[j].N, K)) || overlap(y, w4_scale_range(out[j].sw, out[j].N, K)) ||
+          (i != j && overlap(y, other)))
+        return MLA_ERR_INVALID_ARG;
+    }
+  }
+  if (K > MLA_W4_MAX_K) return MLA_ERR_UNSUPPORTED;
+  int* st = status_ptr();
+  if (st == nullptr) return MLA_ERR_CUDA;
+  W4Params p{};
+  p.x = x;
+  p.sx = x_scale;
+  for (int i = 0; i < n; ++i) p.out[i] = out[i];
+  p.status = st;
+  p.T = T;
+  p.K = K;
+  p.groups = w4_groups(K);
+  return from_cuda(launch_linear_w4(p, stream));
 }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -380,21 +400,30 @@ mla_status mla_dequantize_w4(const uint8_t* w4, const mla_bf16* w_scale, mla_bf1
 
 mla_status mla_linear_w4(const mla_bf16* x, const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* y, int T, int K,
                          int N, cudaStream_t stream) {
-  const mla_status s = linear_w4_check(x, 2, nullptr, w4, w_scale, y, T, K, N);
-  if (s != MLA_OK) return s;
-  int* st = status_ptr();
-  if (st == nullptr) return MLA_ERR_CUDA;
-  return from_cuda(launch_linear_w4(x, nullptr, w4, w_scale, y, T, K, N, st, stream));
+  const W4Out out{w4, w_scale, y, N};
+  return linear_w4(x, 2, nullptr, &out, 1, T, K, stream);
 }
 
 mla_status mla_linear_w4_fp8(const uint8_t* x8, const float* x_scale, const uint8_t* w4, const mla_bf16* w_scale,
                              mla_bf16* y, int T, int K, int N, cudaStream_t stream) {
-  if (!x_scale || !aligned16(x_scale)) return MLA_ERR_INVALID_ARG;
-  const mla_status s = linear_w4_check(x8, 1, x_scale, w4, w_scale, y, T, K, N);
-  if (s != MLA_OK) return s;
-  int* st = status_ptr();
-  if (st == nullptr) return MLA_ERR_CUDA;
-  return from_cuda(launch_linear_w4(x8, x_scale, w4, w_scale, y, T, K, N, st, stream));
+  if (!x_scale) return MLA_ERR_INVALID_ARG;
+  const W4Out out{w4, w_scale, y, N};
+  return linear_w4(x8, 1, x_scale, &out, 1, T, K, stream);
+}
+
+mla_status mla_linear_w4_pair(const mla_bf16* x, int T, int K, const uint8_t* w4_0, const mla_bf16* w_scale_0, int N0,
+                              mla_bf16* y0, const uint8_t* w4_1, const mla_bf16* w_scale_1, int N1, mla_bf16* y1,
+                              cudaStream_t stream) {
+  const W4Out out[2] = {{w4_0, w_scale_0, y0, N0}, {w4_1, w_scale_1, y1, N1}};
+  return linear_w4(x, 2, nullptr, out, 2, T, K, stream);
+}
+
+mla_status mla_linear_w4_fp8_pair(const uint8_t* x8, const float* x_scale, int T, int K, const uint8_t* w4_0,
+                                  const mla_bf16* w_scale_0, int N0, mla_bf16* y0, const uint8_t* w4_1,
+                                  const mla_bf16* w_scale_1, int N1, mla_bf16* y1, cudaStream_t stream) {
+  if (!x_scale) return MLA_ERR_INVALID_ARG;
+  const W4Out out[2] = {{w4_0, w_scale_0, y0, N0}, {w4_1, w_scale_1, y1, N1}};
+  return linear_w4(x8, 1, x_scale, out, 2, T, K, stream);
 }
 
 mla_status mla_read_kv_fp8(const uint8_t* cache_c8, const float* cache_scale, const uint16_t* cache_kr,

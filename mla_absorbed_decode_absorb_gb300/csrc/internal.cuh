@@ -182,9 +182,8 @@ cudaError_t launch_rms_norm(const uint16_t* x, int64_t x_ld, const uint16_t* res
 cudaError_t launch_quantize_w4(const uint16_t* w, uint8_t* w4, uint16_t* scale, int N, int K, cudaStream_t stream);
 cudaError_t launch_dequantize_w4(const uint8_t* w4, const uint16_t* scale, uint16_t* w, int N, int K,
                                  cudaStream_t stream);
-// x: bf16 with x_scale == nullptr, else E4M3 codes
-cudaError_t launch_linear_w4(const void* x, const float* x_scale, const uint8_t* w4, const uint16_t* w_scale,
-                             uint16_t* y, int T, int K, int N, int* status, cudaStream_t stream);
+struct W4Params;  // csrc/w4.cuh
+cudaError_t launch_linear_w4(W4Params p, cudaStream_t stream);
 cudaError_t launch_read_kv_fp8(const uint8_t* c8, const float* scale, const uint16_t* kr, int64_t num_pages,
                                const int32_t* page_table, int pt_stride, const int32_t* kv_lens, int B,
                                int max_kv_len, uint16_t* rows, int* status, cudaStream_t stream);

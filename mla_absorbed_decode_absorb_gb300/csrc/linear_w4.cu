@@ -94,7 +94,9 @@ linear_w4_kernel(const W4Params p) {
   const int lg = lane >> 2, lt = lane & 3;
   const int rw = warp % kRowWarps, kw = warp / kRowWarps;
   const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
-  const int n0 = tile * S::kRows, rw0 = rw * 16 * kM;
+  const bool second = tile >= p.tiles0;
+  const W4Out out = second ? p.out[1] : p.out[0];
+  const int n0 = (tile - (second ? p.tiles0 : 0)) * S::kRows, rw0 = rw * 16 * kM;
   const int t0 = blockIdx.z * kTok;
   const int g0 = rank * p.per + kw, g1 = min(p.groups, rank * p.per + p.per);
   const int ragged = kRagged ? p.groups - 1 : -1;  // the group with 64 columns, if any
@@ -106,8 +108,8 @@ linear_w4_kernel(const W4Params p) {
   int sw_at[2 * kM];
 #pragma unroll
   for (int m = 0; m < 2 * kM; ++m) {
-    const int r = min(n0 + rw0 + 8 * m + lg, p.N - 1);
-    src[m] = p.w4 + r * row_bytes + g0 * 64 + lt * 16;
+    const int r = min(n0 + rw0 + 8 * m + lg, out.N - 1);
+    src[m] = out.w4 + r * row_bytes + g0 * 64 + lt * 16;
     sw_at[m] = r * p.groups;
   }
   const uint32_t ring = smem_u32(smem) + warp * (kM * 1024) + lg * 64;
@@ -136,7 +138,7 @@ linear_w4_kernel(const W4Params p) {
   auto load_sw = [&](int step) {
     const int g = min(g0 + (step + lt) * S::kKWarps, p.groups - 1);
 #pragma unroll
-    for (int m = 0; m < 2 * kM; ++m) next_sw[m] = p.sw[sw_at[m] + g];
+    for (int m = 0; m < 2 * kM; ++m) next_sw[m] = out.sw[sw_at[m] + g];
   };
   load_sw(0);
   if (p.early) grid_dep_wait();
@@ -248,9 +250,9 @@ linear_w4_kernel(const W4Params p) {
   const uint32_t base = smem_u32(part);
   for (int e = rank * kThreads + tid; e < toks * S::kRows; e += p.split * kThreads) {
     const int r = e % S::kRows, t = e / S::kRows;
-    if (n0 + r >= p.N) continue;
+    if (n0 + r >= out.N) continue;
     const float v = sum_partials(base + (t * S::kLd + r) * 4, p.split);
-    p.y[static_cast<int64_t>(t0 + t) * p.N + n0 + r] = f32_to_bf16_bits(v);
+    out.y[static_cast<int64_t>(t0 + t) * out.N + n0 + r] = f32_to_bf16_bits(v);
   }
   if (p.split > 1) cluster_sync();  // peers may still be reading this CTA's partial
 }
@@ -267,7 +269,9 @@ cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  const int tiles = (p.N + S::kRows - 1) / S::kRows, slices = (p.T + kTok - 1) / kTok;
+  const int64_t tiles = p.tiles(S::kRows);
+  const int slices = (p.T + kTok - 1) / kTok;
+  p.tiles0 = (p.out[0].N + S::kRows - 1) / S::kRows;
   // K over a cluster while its CTAs still fit the GPU at once and a warp keeps more than one group (7168 -> 576, one
   // token: 3.6 us in four, against 4.8 undivided and 3.7 in eight)
   p.split = 1;
@@ -276,7 +280,7 @@ cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
       p.split *= 2;
   p.per = (p.groups + p.split - 1) / p.split;
   p.early = launch_overlap() >= 2;
-  return launch_w4(kernel, dim3(tiles * p.split, 1, (p.T + kTok - 1) / kTok), kThreads, S::kRing, stream, p.split, p);
+  return launch_w4(kernel, dim3(static_cast<unsigned>(tiles) * p.split, 1, slices), kThreads, S::kRing, stream, p.split, p);
 }
 
 template <int kRowWarps, int kM>
@@ -289,16 +293,14 @@ cudaError_t launch_rows(const W4Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_linear_w4(const void* x, const float* x_scale, const uint8_t* w4, const uint16_t* w_scale,
-                             uint16_t* y, int T, int K, int N, int* status, cudaStream_t stream) {
-  const W4Params p{x, x_scale, w4, w_scale, y, status, T, K, N, w4_groups(K), 1, 0, false};
-  const int slices = (T + kTok - 1) / kTok;
-  const int64_t tiles = static_cast<int64_t>((N + 15) / 16) * slices;
+cudaError_t launch_linear_w4(W4Params p, cudaStream_t stream) {
+  const int slices = (p.T + kTok - 1) / kTok;
+  const int64_t tiles = p.tiles(16) * slices;
   // Warp MMAs pass over the weights once for 8 tokens, the tensor-core kernel once for 16 to 64 but with a longer way
   // from weight to result: it wins from two passes on once they are over about 36 M weights (1536 x 16384: 17 tokens
   // 11.2 us against 12.8, 16 tokens 9.9 against 9.5; 16384 x 7168: 16 tokens 26 against 32, 64 tokens 33 against
   // 94; but 7168 x 576: 64 tokens 9.8 against 7.4, 512 x 512: 7.1 against 2.4).
-  if (slices > 1 && static_cast<int64_t>(N) * K * slices > 36000000) return launch_linear_w4_tc(p, stream);
+  if (slices > 1 && (static_cast<int64_t>(p.out[0].N) + p.out[1].N) * p.K * slices > 36000000) return launch_linear_w4_tc(p, stream);
   // Up to one wave of CTAs, 16 rows each and K over all eight warps: the latency of few, short streams counts.
   // Beyond, 32 rows a warp share what it unpacks of x (1536 -> 16384, one token: 6.6 us against 7.4), and fewer warps
   // share K where it is short.

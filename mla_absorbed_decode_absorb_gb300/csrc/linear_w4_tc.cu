@@ -76,7 +76,8 @@ struct TcShape {
 
 template <int kTn, bool kFp8>
 __global__ void __launch_bounds__(TcShape<kTn, kFp8>::kThreads, TcShape<kTn, kFp8>::kPerSm)
-linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const W4Params p) {
+linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
+                    const __grid_constant__ CUtensorMap tm_x, const W4Params p) {
   using S = TcShape<kTn, kFp8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -87,7 +88,10 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
-  const int n0 = tile * kRows, t0 = blockIdx.z * kTn;
+  const bool second = tile >= p.tiles0;
+  const W4Out out = second ? p.out[1] : p.out[0];
+  const CUtensorMap* tm_w = second ? &tm_w1 : &tm_w0;
+  const int n0 = (tile - (second ? p.tiles0 : 0)) * kRows, t0 = blockIdx.z * kTn;
   const int g0 = rank * p.per, ng = max(0, min(p.groups, g0 + p.per) - g0);
   volatile int* abort = &bars.abort;
 
@@ -191,7 +195,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
         if (i >= ng) return;
         const uint32_t bar = smem_u32(&bars.weights[i % kStages]);
         mbar_arrive_expect_tx(bar, kSlot);
-        tma_load_2d(smem_u32(ring + (i % kStages) * kSlot), &tm_w, (g0 + i) * 64, n0, bar);
+        tma_load_2d(smem_u32(ring + (i % kStages) * kSlot), tm_w, (g0 + i) * 64, n0, bar);
       };
       // ... and their x: free again once its MMAs have completed
       auto fetch_x = [&](int i) {
@@ -249,7 +253,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
 #pragma unroll
     for (int t = 0; t < S::kEpTok; ++t) acc[t] = 0.f;
     constexpr int kLoad = kTn < 64 ? 16 : 8;  // columns at a time: 64 sums leave few registers
-    const uint16_t* sw = p.sw + static_cast<int64_t>(min(n0 + r, p.N - 1)) * p.groups + g0;
+    const uint16_t* sw = out.sw + static_cast<int64_t>(min(n0 + r, out.N - 1)) * p.groups + g0;
     uint16_t next[4];  // a thread's scales are two bytes of a row of its own: four groups ahead
 #pragma unroll
     for (int q = 0; q < 4; ++q) next[q] = q < ng ? sw[q] : uint16_t(0);
@@ -307,9 +311,9 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
   const uint32_t base = smem_u32(part);
   for (int e = rank * S::kThreads + tid; e < toks * kRows; e += p.split * S::kThreads) {
     const int r = e % kRows, t = e / kRows;
-    if (n0 + r >= p.N) continue;
+    if (n0 + r >= out.N) continue;
     const float v = sum_partials(base + (t * S::kLd + r) * 4, p.split);
-    p.y[static_cast<int64_t>(t0 + t) * p.N + n0 + r] = f32_to_bf16_bits(v);
+    out.y[static_cast<int64_t>(t0 + t) * out.N + n0 + r] = f32_to_bf16_bits(v);
   }
   if (p.split > 1) cluster_sync();  // peers may still be reading this CTA's partial
 }
@@ -329,7 +333,8 @@ cudaError_t launch_tn(W4Params p, cudaStream_t stream) {
   // K over the largest cluster whose CTAs still fit the GPU at once (a second, partial wave costs more: 256 tokens,
   // 7168 -> 1536 in 24 tiles: 14.0 us in clusters of 5, 24.1 in clusters of 6, which do not all fit) and that leaves a
   // CTA two groups, or seven where CTAs share an SM (32 tokens, 1536 -> 16384: 10.4 us undivided, 11.7 halved)
-  const int64_t tiles = (p.N + kRows - 1) / kRows, slices = (p.T + kTn - 1) / kTn;
+  const int64_t tiles = p.tiles(kRows), slices = (p.T + kTn - 1) / kTn;
+  p.tiles0 = (p.out[0].N + kRows - 1) / kRows;
   static int fit[kMaxDevicesLocal][kW4MaxSplit + 1] = {};  // clusters resident at once, 0: not asked yet
   p.split = 1;
   for (int s = kW4MaxSplit; s > 1; --s) {
@@ -349,13 +354,17 @@ cudaError_t launch_tn(W4Params p, cudaStream_t stream) {
   }
   p.per = (p.groups + p.split - 1) / p.split;
   p.early = launch_overlap() >= 2;
-  CUtensorMap tm_w, tm_x;
-  if (!make_tmap_u8_2d(&tm_w, p.w4, p.N, p.K / 2, p.K / 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_64B))
-    return cudaErrorInvalidValue;
+  CUtensorMap tm_w[2], tm_x;
+  for (int i = 0; i < 2; ++i) {
+    const W4Out& o = p.out[i].N > 0 ? p.out[i] : p.out[0];  // (not read without a second projection)
+    if (!make_tmap_u8_2d(&tm_w[i], o.w4, o.N, p.K / 2, p.K / 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
   const bool ok = kFp8 ? make_tmap_u8_2d(&tm_x, p.x, p.T, p.K, p.K, kW4Group, kTn, CU_TENSOR_MAP_SWIZZLE_128B)
                        : make_tmap_bf16_2d(&tm_x, p.x, p.T, p.K, p.K, 64, kTn, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
-  return launch_w4(kernel, dim3(static_cast<unsigned>(tiles) * p.split, 1, static_cast<unsigned>(slices)), S::kThreads, S::kSmem, stream, p.split, tm_w, tm_x, p);
+  return launch_w4(kernel, dim3(static_cast<unsigned>(tiles) * p.split, 1, static_cast<unsigned>(slices)), S::kThreads, S::kSmem, stream, p.split,
+                   tm_w[0], tm_w[1], tm_x, p);
 }
 
 template <bool kFp8>

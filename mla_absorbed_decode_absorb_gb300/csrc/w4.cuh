@@ -72,16 +72,28 @@ __device__ __forceinline__ void w4_pairs_f16(uint32_t v, uint32_t (&p)[4]) {
 // ------------------------------------------------------------------ projections
 constexpr int kW4MaxSplit = 8;  // CTAs of a cluster along K (the portable size)
 
-struct W4Params {
-  const void* x;        // bf16 [T, K] or E4M3 [T, K]
-  const float* sx;      // [T, groups] (E4M3 x)
+// One projection's weight and output.
+struct W4Out {
   const uint8_t* w4;    // [N, K / 2]
   const uint16_t* sw;   // [N, groups] bf16
   uint16_t* y;          // [T, N] bf16
+  int N;
+};
+
+struct W4Params {
+  const void* x;        // bf16 [T, K] or E4M3 [T, K]
+  const float* sx;      // [T, groups] (E4M3 x)
+  W4Out out[2];         // one projection of x, or two (out[1].N > 0) in one launch
   int* status;
-  int T, K, N, groups;
+  int T, K, groups;
+  int tiles0;           // tiles of the first projection: CTA tiles from there on compute the second
   int split, per;       // CTAs along K, groups per CTA
   bool early;           // the weights may be read before the previous kernel has finished
+
+  // Tiles of `rows` features of both projections, in order.
+  __host__ int64_t tiles(int rows) const {
+    return (static_cast<int64_t>(out[0].N) + rows - 1) / rows + (static_cast<int64_t>(out[1].N) + rows - 1) / rows;
+  }
 };
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {

@@ -66,6 +66,8 @@ _SIGS = {
     "mla_dequantize_w4": ([_p, _p, _p, _i, _i, _p], _i),
     "mla_linear_w4": ([_p, _p, _p, _p, _i, _i, _i, _p], _i),
     "mla_linear_w4_fp8": ([_p, _p, _p, _p, _p, _i, _i, _i, _p], _i),
+    "mla_linear_w4_pair": ([_p, _i, _i, _p, _p, _i, _p, _p, _p, _i, _p, _p], _i),
+    "mla_linear_w4_fp8_pair": ([_p, _p, _i, _i, _p, _p, _i, _p, _p, _p, _i, _p, _p], _i),
     "mla_read_kv_fp8": ([_p, _p, _p, _i64, _p, _i, _p, _i, _i, _p, _p], _i),
     "mla_rope_q": ([_p, _p, _p, _i, _p, _i, _i, _p], _i),
     "mla_f32_to_bf16": ([_p, _p, _i64, _p], _i),
@@ -367,6 +369,40 @@ def mla_linear_w4_fp8(x8, x_scale, w4, w_scale, y=None, stream=None):
         _arg(w4, "w4", torch.uint8, (N, K // 2), dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, groups), dev),
         _arg(y, "y", torch.bfloat16, (T, N), dev), T, K, N, _stream(stream, dev)))
     return y
+
+
+def _w4_pair(x, w0, w1, y0, y1, T, K, dev):
+    args, ys = [], []
+    for name, (w4, w_scale), y in (("0", w0, y0), ("1", w1, y1)):
+        N = w4.shape[0]
+        if y is None:
+            y = _new((T, N), torch.bfloat16, x)
+        ys.append(y)
+        args += [_arg(w4, "w4_" + name, torch.uint8, (N, K // 2), dev),
+                 _arg(w_scale, "w_scale_" + name, torch.bfloat16, (N, _groups(K)), dev), N,
+                 _arg(y, "y" + name, torch.bfloat16, (T, N), dev)]
+    return args, tuple(ys)
+
+
+def mla_linear_w4_pair(x, w0, w1, y0=None, y1=None, stream=None):
+    """``y0 = x w0^T`` and ``y1 = x w1^T`` in one launch, each weight a (w4, w_scale) pair."""
+    T, K = shape = x.shape
+    dev = _device()
+    args, ys = _w4_pair(x, w0, w1, y0, y1, T, K, dev)
+    _check("mla_linear_w4_pair", lib.mla_linear_w4_pair(
+        _arg(x, "x", torch.bfloat16, shape, dev), T, K, *args, _stream(stream, dev)))
+    return ys
+
+
+def mla_linear_w4_fp8_pair(x8, x_scale, w0, w1, y0=None, y1=None, stream=None):
+    """:func:`mla_linear_w4_pair` of 8-bit activations as :func:`mla_rms_norm_fp8` returns them."""
+    T, K = shape = x8.shape
+    dev = _device()
+    args, ys = _w4_pair(x8, w0, w1, y0, y1, T, K, dev)
+    _check("mla_linear_w4_fp8_pair", lib.mla_linear_w4_fp8_pair(
+        _arg(x8, "x8", torch.uint8, shape, dev), _arg(x_scale, "x_scale", torch.float32, (T, _groups(K)), dev), T, K,
+        *args, _stream(stream, dev)))
+    return ys
 
 
 def mla_read_kv_fp8(cache_fp8, page_table, kv_lens, max_kv_len, rows=None, stream=None):

@@ -453,18 +453,23 @@ class LayerSession:
         else:
             ops.mla_linear(x, w, y, self.ws, stream)
 
+    def _pair(self, x, w0, w1, y0, y1, stream):
+        """Two projections of one input: one launch."""
+        if isinstance(x, tuple):
+            ops.mla_linear_w4_fp8_pair(*x, w0, w1, y0, y1, stream=stream)
+        elif self.weights == "w4":
+            ops.mla_linear_w4_pair(x, w0, w1, y0, y1, stream=stream)
+        else:
+            ops.mla_linear_pair(x, w0, w1, y0, y1, self.ws, stream)
+
     def norm_in(self, stream=None):
         self._norm(self.x, self.norms.hidden, self._x_normed, stream, self.residual)
 
     def proj_kv(self, stream=None):
         x = self.x if self.norms is None else self._x_normed
         c_kv = self._c_new if self.norms is None else self.c_kv
-        if self.weights == "w4":
-            self._linear(x, self.w_dkv, c_kv, stream)
-            self._linear(x, self.w_kr, self._k_new, stream)
-        else:
-            # W_DKV and W_KR read the same hidden state: one launch
-            ops.mla_linear_pair(x, self.w_dkv, self.w_kr, c_kv, self._k_new, self.ws, stream)
+        # W_DKV and W_KR read the same hidden state
+        self._pair(x, self.w_dkv, self.w_kr, c_kv, self._k_new, stream)
         if self.norms is not None:
             ops.mla_rms_norm(self.c_kv, self.norms.kv_latent, self.norms.eps, y=self._c_new, stream=stream)
 
@@ -479,6 +484,9 @@ class LayerSession:
             ops.mla_linear_strided(c_q, self.w_qk, d.q_abs, N_HEADS * D_ROW, D_LATENT, D_ROW, self.ws, stream)
             ops.mla_linear(c_q, self.w_qr, self._q_rope, self.ws, stream)
             ops.mla_rope_q(d.q_rope, d.prior_lens, d.rope, d.q_abs, stream=stream)
+            return
+        if self.weights == "w4":
+            self._pair(c_q, self.w_uq, self.w_qr, self._q_nope, self._q_rope, stream)
             return
         self._linear(c_q, self.w_uq, self._q_nope, stream)
         self._linear(c_q, self.w_qr, self._q_rope, stream)
@@ -526,7 +534,7 @@ class LayerSession:
         if self.norms is not None:
             n += 3
         if self.weights == "w4":
-            return n + 2 + len(lin)  # one launch each, W_DKV and W_KR among them
+            return n + 4  # W_DKV and W_KR, W_DQ, W_UQ and W_QR, W_O
         for w, k in lin:
             n += 1 + (1 if ops.mla_linear_workspace_size(self.T, k, w.shape[0]) else 0)
         # W_DKV and W_KR in one launch (plus its split-K sum)

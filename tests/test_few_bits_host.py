@@ -103,6 +103,8 @@ def lib():
     lib.mla_dequantize_w4.argtypes = [P, P, P, I, I, P]
     lib.mla_linear_w4.argtypes = [P, P, P, P, I, I, I, P]
     lib.mla_linear_w4_fp8.argtypes = [P, P, P, P, P, I, I, I, P]
+    lib.mla_linear_w4_pair.argtypes = [P, I, I, P, P, I, P, P, P, I, P, P]
+    lib.mla_linear_w4_fp8_pair.argtypes = [P, P, I, I, P, P, I, P, P, P, I, P, P]
     lib.mla_read_kv_fp8.argtypes = [P, P, P, I64, P, I, P, I, I, P, P]
     return lib
 
@@ -155,6 +157,17 @@ def test_w4_refusals(lib):
     assert lib.mla_linear_w4_fp8(x, None, w4, s, y, 2, 128, 4, None) == INVALID
     assert lib.mla_linear_w4_fp8(x, at(4) + 4, w4, s, y, 2, 128, 4, None) == INVALID
     assert lib.mla_linear_w4_fp8(x, y + 4, w4, s, y, 2, 128, 4, None) == INVALID
+    assert lib.mla_linear_w4(x, w4, s, y, 2, 4194304 + 64, 4, None) == UNSUPPORTED
+    good = [x, 2, 128, w4, s, 4, y, at(5), at(6), 6, at(7), None]
+    for i, bad in [(0, None), (1, 0), (1, 257), (2, 96), (3, None), (4, None), (5, 0), (6, None), (7, None), (8, None),
+                   (9, 0), (10, None), (0, x + 8), (3, w4 + 8), (7, at(5) + 8), (8, at(6) + 8), (10, at(7) + 1),
+                   (10, y + 8), (6, at(5)), (10, w4), (10, x), (6, at(6))]:
+        a = list(good)
+        a[i] = bad
+        assert lib.mla_linear_w4_pair(*a) == INVALID, (i, bad)
+        assert lib.mla_linear_w4_fp8_pair(a[0], at(9), *a[1:]) == INVALID, (i, bad)
+    assert lib.mla_linear_w4_fp8_pair(good[0], None, *good[1:]) == INVALID
+    assert lib.mla_linear_w4_fp8_pair(good[0], y, *good[1:]) == INVALID
 
 
 def test_read_refusals(lib):

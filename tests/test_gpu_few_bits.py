@@ -242,6 +242,27 @@ def test_linear_parity_large(T, K, N, fp8):
     ok()
 
 
+@pytest.mark.parametrize("T,K,N0,N1", [(1, 7168, 512, 64), (3, 192, 17, 1), (8, 1088, 1, 700), (5, 128, 9000, 9001),
+                                       (32, 1536, 5000, 2600), (16, 192, 50001, 47000), (64, 704, 3000, 5001),
+                                       (100, 1088, 1300, 1301), (256, 64, 8000, 9700)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_linear_pair_parity(T, K, N0, N1, fp8):
+    """Two projections of one x in one launch, in both kernels; the second one's rows stay its own."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    x, sx, w4, scale = linear_inputs(T, K, N0, fp8, T + K)
+    _, _, w4b, scale_b = linear_inputs(T, K, N1, fp8, T + K + 1)
+    w0, w1 = (w4.cuda(), scale.cuda()), (w4b.cuda(), scale_b.cuda())
+    if fp8:
+        y0, y1 = ops.mla_linear_w4_fp8_pair(x.cuda(), sx.cuda(), w0, w1)
+    else:
+        y0, y1 = ops.mla_linear_w4_pair(x.cuda(), w0, w1)
+    for y, w, s in ((y0, w4, scale), (y1, w4b, scale_b)):
+        ref, tol = linear_ref(x, sx, w, s)
+        assert y.shape == ref.shape
+        within(f64(y), ref, tol)
+    ok()
+
+
 @pytest.mark.parametrize("T,N", [(8, 500), (16, 150000), (48, 50000), (64, 36000), (256, 9300)])
 def test_linear_keeps_what_cancels(T, N):
     """Pairs of columns with one x (2 .. 30) and weights c and -c, and one column of the smallest E4M3 value 2^-9,
