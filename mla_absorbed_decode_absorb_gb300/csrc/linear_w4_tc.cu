@@ -300,11 +300,13 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
 #pragma unroll
     for (int t = 0; t < S::kEpTok; ++t) part[(c0 + t) * S::kLd + r] = acc[t];
   }
+  // TMEM goes back before any wait for a peer: kernels on two streams, each waiting in a cluster with TMEM that the
+  // other's CTAs need to start, would wait for ever
   tc_fence_before();
-  if (p.split > 1) cluster_sync();
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   if (warp == S::kIssuer) tmem_dealloc(tmem, S::kTmemCols);
+  if (p.split > 1) cluster_sync();
 
   // the cluster's threads share the (token, row) sums, row fastest, each in rank order
   const int toks = min(kTn, p.T - t0);

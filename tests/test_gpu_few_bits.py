@@ -497,6 +497,24 @@ def test_two_calls_at_once():
     assert all(torch.equal(t.view(torch.int16), rb.view(torch.int16)) for t in yb)
 
 
+def test_two_tensor_core_calls_at_once():
+    """Clusters of two launches share SMs and their tensor memory: both finish, with the results of either alone.
+    Up to 64 tokens a CTA holds 256 columns of its SM's tensor memory, beyond 512."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    shapes = ((40, 7168, 1536), (128, 7168, 577), (64, 16384, 900), (256, 7168, 576))
+    args = [[t if t is None else t.cuda() for t in linear_inputs(T, K, N, False, T)] for T, K, N in shapes]
+    ref = [ops.mla_linear_w4(a[0], a[2], a[3]) for a in args]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    out = [[torch.empty_like(r) for _ in range(8)] for r in ref]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for a, y, s in zip(args, out, streams):
+            ops.mla_linear_w4(a[0], a[2], a[3], y[i], stream=s)
+    ok()
+    for r, ys in zip(ref, out):
+        assert all(torch.equal(y.view(torch.int16), r.view(torch.int16)) for y in ys)
+
+
 def test_read_back_feeds_the_non_absorbed_path():
     """FP8 append, read back, decompress: keys and values of the dequantised cache rows."""
     from mla_absorbed_decode_absorb_gb300 import ops
