@@ -108,7 +108,20 @@ rms_norm_kernel(const NormParams p) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(p.D)) + p.eps));
+  // The factor's power of two goes into h at once (exact), what is left is in [1, 2): h w alone could leave fp32's range
+  // where v does not.  An infinity or a NaN stays whole.
+  float inv = __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(p.D)) + p.eps));
+  float power = __uint_as_float(__float_as_uint(inv) & 0x7f800000u);
+  if (power == __uint_as_float(0x7f800000u)) {
+    power = inv;
+    inv = 1.f;
+  } else {
+    inv = __uint_as_float((__float_as_uint(inv) & 0x007fffffu) | 0x3f800000u);
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[i][e] *= power;
 
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
@@ -168,7 +181,7 @@ cudaError_t launch_rms_norm(const uint16_t* x, int64_t x_ld, const uint16_t* res
   if (chunks <= 64 && T >= 1024) return launch_shape<2, 256, 32>(p, stream);
   // one chunk per thread while the rows fit the GPU at once (32 x 1536: 1.8 us, against 2.1 with two chunks;
   // 128 x 7168: 3.4 against 3.9), then two, which keep twice the bytes in flight per register (16384 x 7168 with
-  // the residual, 8-bit output: 120 us against 155, 1.02 of the measured copy bandwidth; four chunks: 122)
+  // the residual, 8-bit output: 123 us against 155, 0.99 of the measured copy bandwidth; four chunks: 122)
   if (chunks <= 1024 && static_cast<int64_t>(T) * chunks <= 152 * 2048) return launch_shape<1, 1024, 0>(p, stream);
   if (chunks <= 1024) return launch_shape<2, 512, 0>(p, stream);
   return launch_shape<4, 512, 0>(p, stream);  // up to 16384 columns (8192 rows: 156 us, 1.01)

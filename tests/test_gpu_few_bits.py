@@ -130,6 +130,22 @@ def test_norm_rows_of_zeros_and_non_finite_rows():
     ok()
 
 
+@pytest.mark.parametrize("xe,we", [(-50, -80), (-50, 100), (50, -100), (50, 100), (0, -100), (0, 120)])
+def test_norm_of_small_and_large_values(xe, we):
+    """Rows of about 2^xe times a weight of about 2^we, whose product may leave fp32's range where v does not: v in
+    both forms, and the scale's floor of 2^-100 below it."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    x, r, w = norm_inputs(5, 384, 77)
+    x, r, w = x * 2.0 ** xe, r * 2.0 ** xe, w * 2.0 ** we
+    x[:, 5], r[:, 5] = 0, 0
+    for res in (None, r):
+        out = None if res is None else torch.empty_like(res)
+        check_norm(x, res, w, 0.0, r_out=out, y=ops.mla_rms_norm(x, w, 0.0, res, out))
+        y8, s = ops.mla_rms_norm_fp8(x, w, 0.0, res, out)
+        check_norm(x, res, w, 0.0, y8=y8, scale=s)
+    ok()
+
+
 def test_norm_of_no_rows_and_refusals():
     from mla_absorbed_decode_absorb_gb300 import ops
     x, r, w = norm_inputs(4, 256, 9)
