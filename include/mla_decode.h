@@ -505,11 +505,12 @@ mla_status mla_rms_norm(const mla_bf16* x, int64_t x_ld, const mla_bf16* residua
  * applied to each group's sum in float32, and y is rounded once.  K is split
  * over the CTAs of a cluster, whose partials are added in a fixed order on
  * chip: no workspace, and a result that does not depend on timing.
- * N >= 1, K >= 64 a multiple of 64; the projections take K <= MLA_W4_MAX_K
- * (MLA_ERR_UNSUPPORTED beyond); an output must not overlap an input or the other.
+ * 1 <= N <= MLA_W4_MAX_N, K a multiple of 64, 64 .. MLA_W4_MAX_K, and N * ceil(K / 128)
+ * below 2^31 (MLA_ERR_UNSUPPORTED beyond); an output must not overlap an input or the other.
  */
 #define MLA_W4_GROUP 128
 #define MLA_W4_MAX_K 4194304
+#define MLA_W4_MAX_N 1073741824
 mla_status mla_quantize_w4(const mla_bf16* w, uint8_t* w4, mla_bf16* w_scale, int N, int K, cudaStream_t stream);
 mla_status mla_dequantize_w4(const uint8_t* w4, const mla_bf16* w_scale, mla_bf16* w, int N, int K,
                              cudaStream_t stream);
@@ -583,9 +584,9 @@ mla_status mla_copy_async(void* dst, const void* src, size_t bytes, cudaStream_t
  *      barriers and tensor memory; it reads or writes global memory only after
  *      that kernel has completed and its writes are visible.  Same results and
  *      the same ordering guarantees as 0.
- *   2  as 1, and the weight matrices w_uk (mla_absorb_q) and w_uv
- *      (mla_out_absorb, mla_combine_out_absorb) are read BEFORE the previous
- *      kernel has completed.  Only valid while no work still running on the
+ *   2  as 1, and the weight matrices w_uk (mla_absorb_q), w_uv
+ *      (mla_out_absorb, mla_combine_out_absorb) and w4 with w_scale (the
+ *      mla_linear_w4 calls) are read BEFORE the previous kernel has completed.  Only valid while no work still running on the
  *      stream writes those weights (fixed inference weights).  Likewise
  *      mla_copy_async reads a host-memory source before that point.
  *

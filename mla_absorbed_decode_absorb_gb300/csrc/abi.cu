@@ -69,8 +69,10 @@ Range w4_scale_range(const mla_bf16* s, int N, int K) {
 mla_status w4_check(const uint8_t* w4, const mla_bf16* w_scale, int N, int K) {
   if (N < 1 || K < 64 || K % 64 != 0 || !w4 || !w_scale || !aligned16(w4) || !aligned16(w_scale))
     return MLA_ERR_INVALID_ARG;
-  // a weight's groups are counted in 32 bits
-  if (static_cast<int64_t>(N) * ((K + MLA_W4_GROUP - 1) / MLA_W4_GROUP) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  // a weight's groups, and its rows rounded up to a tile's, are counted in 32 bits
+  if (K > MLA_W4_MAX_K || N > MLA_W4_MAX_N ||
+      static_cast<int64_t>(N) * ((K + MLA_W4_GROUP - 1) / MLA_W4_GROUP) > INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
 
@@ -95,7 +97,6 @@ mla_status linear_w4(const void* x, int x_elem, const float* x_scale, const W4Ou
         return MLA_ERR_INVALID_ARG;
     }
   }
-  if (K > MLA_W4_MAX_K) return MLA_ERR_UNSUPPORTED;
   int* st = status_ptr();
   if (st == nullptr) return MLA_ERR_CUDA;
   W4Params p{};

@@ -140,6 +140,8 @@ def test_w4_refusals(lib):
         assert f(at(0), at(1), at(2), 4, 96, None) == INVALID
         assert f(at(0), at(1), at(2), 4, 0, None) == INVALID
         assert f(at(0), at(1), at(2), 2 ** 30, 512, None) == UNSUPPORTED  # 2^32 groups
+        assert f(at(0), at(1), at(2), 1, 2 ** 31 - 64, None) == UNSUPPORTED
+        assert f(at(0), at(1), at(2), 2 ** 31 - 1, 64, None) == UNSUPPORTED
         for i in range(3):
             for bad in (None, at(i) + 8):
                 a = [at(0), at(1), at(2)]
@@ -157,7 +159,8 @@ def test_w4_refusals(lib):
     assert lib.mla_linear_w4_fp8(x, None, w4, s, y, 2, 128, 4, None) == INVALID
     assert lib.mla_linear_w4_fp8(x, at(4) + 4, w4, s, y, 2, 128, 4, None) == INVALID
     assert lib.mla_linear_w4_fp8(x, y + 4, w4, s, y, 2, 128, 4, None) == INVALID
-    assert lib.mla_linear_w4(x, w4, s, y, 2, 4194304 + 64, 4, None) == UNSUPPORTED
+    for K, N in [(4194304 + 64, 4), (2 ** 31 - 64, 4), (64, 2 ** 30 + 1), (64, 2 ** 31 - 1)]:
+        assert lib.mla_linear_w4(0x1000, 1 << 60, 1 << 61, 1 << 62, 1, K, N, None) == UNSUPPORTED
     good = [x, 2, 128, w4, s, 4, y, at(5), at(6), 6, at(7), None]
     for i, bad in [(0, None), (1, 0), (1, 257), (2, 96), (3, None), (4, None), (5, 0), (6, None), (7, None), (8, None),
                    (9, 0), (10, None), (0, x + 8), (3, w4 + 8), (7, at(5) + 8), (8, at(6) + 8), (10, at(7) + 1),
