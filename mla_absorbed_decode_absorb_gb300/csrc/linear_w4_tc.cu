@@ -28,21 +28,18 @@ namespace {
 using namespace sm100;
 
 constexpr int kRows = 128;
-constexpr int kStages = 4;                     // groups of weights in flight or in use
 constexpr int kSlot = kRows * 64;              // a group of weights
-constexpr int kRing = kStages * kSlot;
 constexpr int kMaxCtas = 304;                  // two on each of 152 SMs: more never run at once
-constexpr uint32_t kTmemA = 0;                 // two operands of 64 columns, then two accumulators
-constexpr uint32_t kTmemD = 128;
+constexpr int kSxStages = 8;                   // groups of x's scales: the producers are at most six groups ahead of the sums
 
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&d)[16]) { tmem_ld16(at, d); }
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&d)[8]) { tmem_ld8(at, d); }
 
 struct Bars {
-  uint64_t weights[kStages];  // a group of weights has landed (TMA)
-  uint64_t x[4];              // a group of x has landed (TMA)
-  uint64_t ready[2];    // a group's weights (and x's scales) are in place (one arrival per producer warp)
-  uint64_t free[2];     // ... and have been consumed, and its x (commit)
+  uint64_t weights[8];  // a group of weights has landed (TMA)
+  uint64_t x[4];        // a group of x has landed (TMA)
+  uint64_t ready[4];    // a group's weights (and x's scales) are in place (one arrival per producer warp)
+  uint64_t free[4];     // ... and have been consumed, and its x (commit)
   uint64_t full[2];     // a group's accumulator is complete (commit)
   uint64_t drained[2];  // ... and has been read (one arrival per epilogue warp)
   uint32_t tmem;
@@ -60,16 +57,22 @@ struct TcShape {
   // 26.2); 64 sums and x's scales in pairs spill (256 tokens in 8 bits: 140 us against 95).
   static constexpr bool kPacked = kEpTok < 64 || (kTn == 128 && !kFp8);
   static constexpr int kIssuer = kEpilogue + kEpWarps;         // first of the two warps that issue MMAs
+  static constexpr int kACols = kFp8 ? 32 : 64;                // TMEM columns of a group's weights
+  static constexpr int kABufs = kFp8 || kTn > 64 ? 4 : 2;      // ... in place or in use, in front of two accumulators
+  static constexpr uint32_t kTmemD = kABufs * kACols;
   static constexpr int kDCols = kTn <= 64 ? 64 : 128;          // TMEM columns of an accumulator
   static constexpr uint32_t kTmemCols = kTn <= 64 ? 256 : 512;
-  static constexpr int kThreads = 32 * (kIssuer + 2);
+  static constexpr bool kLoader = kTn > 64;                    // x is fetched by a warp of its own
+  static constexpr int kThreads = 32 * (kIssuer + 2 + (kLoader ? 1 : 0));
+  static constexpr int kStages = kTn <= 64 || !kFp8 ? 4 : 8;   // groups of weights in flight or in use
+  static constexpr int kRing = kStages * kSlot;
   static constexpr int kBox = kTn * 128;                       // kTn tokens x 64 columns (bf16) or 128 (E4M3)
   static constexpr int kB = kFp8 ? kBox : 2 * kBox;            // a group of x
   static constexpr int kXStages = 4;                           // groups of x in flight or in use
   static constexpr int kLd = kRows + 4;                        // floats per token of a partial
   static constexpr int kPart = kTn * kLd * 4;                  // the CTA's partial, over the operands
   static constexpr int kBody = kXStages * kB + kRing > kPart ? kXStages * kB + kRing : kPart;
-  static constexpr int kSx = kFp8 ? 4 * kTn * 4 : 0;           // scales of x, four groups
+  static constexpr int kSx = kFp8 ? kSxStages * kTn * 4 : 0;   // scales of x
   static constexpr int kSmem = kBody + kSx + 256 + 1024;
   static_assert(sizeof(Bars) <= 256, "barrier block");
 };
@@ -82,7 +85,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + S::kXStages * S::kB;
-  float* sxs = reinterpret_cast<float*>(smem + S::kBody);  // [4][kTn]
+  float* sxs = reinterpret_cast<float*>(smem + S::kBody);  // [kSxStages][kTn]
   Bars& bars = *reinterpret_cast<Bars*>(smem + S::kBody + S::kSx);
   float* part = reinterpret_cast<float*>(smem);
 
@@ -96,11 +99,13 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
   volatile int* abort = &bars.abort;
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars.weights[i]), 1);
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars.x[i]), 1);
+    for (int i = 0; i < S::kStages; ++i) mbar_init(smem_u32(&bars.weights[i]), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&bars.x[i]), 1);
+      mbar_init(smem_u32(&bars.ready[i]), 4);
+      mbar_init(smem_u32(&bars.free[i]), 1);
+    }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&bars.ready[b]), 4);
-      mbar_init(smem_u32(&bars.free[b]), 1);
       mbar_init(smem_u32(&bars.full[b]), 1);
       mbar_init(smem_u32(&bars.drained[b]), S::kEpWarps);
     }
@@ -118,6 +123,19 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
   if (!p.early || warp < S::kIssuer) grid_dep_wait();  // the issuers fetch weights
   grid_dep_launch();
 
+  // A group of x: its place is free again once its MMAs have completed.
+  auto fetch_x = [&](int i) {
+    if (i >= ng) return;
+    const uint32_t bar = smem_u32(&bars.x[i & 3]), at = smem_u32(smem + (i & 3) * S::kB);
+    mbar_arrive_expect_tx(bar, S::kB);
+    tma_load_2d(at, &tm_x, (g0 + i) * kW4Group, t0, bar);
+    if (!kFp8) tma_load_2d(at + S::kBox, &tm_x, (g0 + i) * kW4Group + 64, t0, bar);
+  };
+  // The group has left its operands: its MMAs have completed.
+  auto wait_free = [&](int i, volatile int* give_up) {
+    return mbar_wait(smem_u32(&bars.free[i & 3]), (i >> 2) & 1, p.status, give_up);
+  };
+
   if (warp < S::kEpilogue) {
     // -------------------------------------------------------------- producers
     // Rows past N and columns past K are zeros, tokens past T read as the last one (not stored).
@@ -132,12 +150,12 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     bool ok = true;
     for (int i = set; i < ng; i += S::kSets) {
-      const int b = i & 1;
-      ok = mbar_wait(smem_u32(&bars.weights[i % kStages]), (i / kStages) & 1, p.status, abort);
+      const int b = i & (S::kABufs - 1);
+      ok = mbar_wait(smem_u32(&bars.weights[i % S::kStages]), (i / S::kStages) & 1, p.status, abort);
       uint32_t w[16];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint4 v = *reinterpret_cast<const uint4*>(wrow + (i % kStages) * kSlot + ((q ^ perm) << 4));
+        const uint4 v = *reinterpret_cast<const uint4*>(wrow + (i % S::kStages) * kSlot + ((q ^ perm) << 4));
         w[4 * q] = v.x;
         w[4 * q + 1] = v.y;
         w[4 * q + 2] = v.z;
@@ -167,23 +185,37 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
       constexpr int kAhead = kTn < 128 ? 0 : kQuarters;
 #pragma unroll
       for (int h = 0; h < kAhead; ++h) unpack(h);
-      if (i >= 2) ok = ok && mbar_wait(smem_u32(&bars.free[b]), ((i >> 1) & 1) ^ 1, p.status, abort);
+      if (i >= S::kABufs) ok = ok && wait_free(i - S::kABufs, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (kFp8) {
-        if (r < kTn) sxs[(i & 3) * kTn + r] = sx;
+        if (r < kTn) sxs[i % kSxStages * kTn + r] = sx;
         load_sx(i + S::kSets);
       }
 #pragma unroll
       for (int h = 0; h < kQuarters; ++h) {
         if (h >= kAhead) unpack(h);
-        tmem_st16(tmem + lane_off + kTmemA + 64 * b + 16 * h, a[h]);
+        tmem_st16(tmem + lane_off + S::kACols * b + 16 * h, a[h]);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.ready[b]));
+      if (lane == 0) mbar_arrive(smem_u32(&bars.ready[i & 3]));
     }
+  } else if (S::kLoader && warp == S::kIssuer + 2) {
+    // -------------------------------------------------------------- x
+    if (lane == 0) {
+      if (p.early) grid_dep_wait();
+      int i = 0;
+      for (; i < ng; ++i) {
+        if (i >= 4 && !wait_free(i - 4, abort)) break;
+        fetch_x(i);
+      }
+      // given up: wait for the copies that may still be in flight
+      for (int j = max(0, i - 4); i < ng && j < i; ++j)
+        mbar_wait(smem_u32(&bars.x[j & 3]), (j >> 2) & 1, p.status);
+    }
+    __syncwarp();
   } else if (warp >= S::kIssuer) {
     // -------------------------------------------------------------- MMA issuers
     // An MMA this narrow holds its issuing thread far longer than the tensor pipe (113 cycles for N <= 128), so
@@ -193,54 +225,52 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
       // the weights of this buffer's groups: a slot is free again once the producers are ready with it
       auto fetch = [&](int i) {
         if (i >= ng) return;
-        const uint32_t bar = smem_u32(&bars.weights[i % kStages]);
+        const uint32_t bar = smem_u32(&bars.weights[i % S::kStages]);
         mbar_arrive_expect_tx(bar, kSlot);
-        tma_load_2d(smem_u32(ring + (i % kStages) * kSlot), tm_w, (g0 + i) * 64, n0, bar);
-      };
-      // ... and their x: free again once its MMAs have completed
-      auto fetch_x = [&](int i) {
-        if (i >= ng) return;
-        const uint32_t bar = smem_u32(&bars.x[i & 3]), at = smem_u32(smem + (i & 3) * S::kB);
-        mbar_arrive_expect_tx(bar, S::kB);
-        tma_load_2d(at, &tm_x, (g0 + i) * kW4Group, t0, bar);
-        if (!kFp8) tma_load_2d(at + S::kBox, &tm_x, (g0 + i) * kW4Group + 64, t0, bar);
+        tma_load_2d(smem_u32(ring + (i % S::kStages) * kSlot), tm_w, (g0 + i) * 64, n0, bar);
       };
       int i = b;
-      for (; i < kStages; i += 2) fetch(i);
-      if (p.early) grid_dep_wait();
-      fetch_x(b);
-      fetch_x(b + 2);
+      for (; i < S::kStages; i += 2) fetch(i);
+      if (!S::kLoader) {
+        if (p.early) grid_dep_wait();
+        fetch_x(b);
+        fetch_x(b + 2);
+      }
       const uint32_t idesc = kFp8 ? idesc_f16(128, kTn, 0, 0) : idesc_bf16(128, kTn, 0, 0);
-      int fetched = i, fetched_x = b + 4;  // first groups of this buffer not fetched yet
+      int issued = -1;                                      // the last group whose MMAs are issued
+      int w_from = b, w_to = i, x_from = b, x_to = b + 4;  // groups whose copies may be in flight
       for (i = b; i < ng; i += 2) {
-        if (i >= 2) {
-          if (!mbar_wait(smem_u32(&bars.free[b]), ((i >> 1) & 1) ^ 1, p.status, abort)) break;
-          fetch_x(fetched_x);
-          fetched_x += 2;
+        if (!S::kLoader && i >= 2) {
+          if (!wait_free(i - 2, abort)) break;
+          fetch_x(x_to);
+          x_to += 2;
         }
-        if (!mbar_wait(smem_u32(&bars.ready[b]), (i >> 1) & 1, p.status, abort)) break;
-        fetch(fetched);
-        fetched += 2;
+        if (!mbar_wait(smem_u32(&bars.ready[i & 3]), (i >> 2) & 1, p.status, abort)) break;
+        w_from = i + 2;
+        fetch(w_to);
+        w_to += 2;
         if (!mbar_wait(smem_u32(&bars.x[i & 3]), (i >> 2) & 1, p.status, abort)) break;
+        x_from = i + 2;
         if (i >= 2 && !mbar_wait(smem_u32(&bars.drained[b]), ((i >> 1) & 1) ^ 1, p.status, abort)) break;
         tc_fence_after();
         const uint32_t b0 = smem_u32(smem + (i & 3) * S::kB);
-        const uint32_t d = tmem + kTmemD + S::kDCols * b, a0 = tmem + kTmemA + 64 * b;
+        const uint32_t d = tmem + S::kTmemD + S::kDCols * b, a0 = tmem + S::kACols * (i & (S::kABufs - 1));
 #pragma unroll
         for (int q = 0; q < (kFp8 ? 4 : 8); ++q) {
           const uint64_t bd = smem_desc(b0 + (q >> 2) * S::kBox + (q & 3) * 32, 16, 1024, kSw128);
           if (kFp8) mma_ts_f8(d, a0 + 8 * q, bd, idesc, q ? 1u : 0u);
           else mma_ts(d, a0 + 8 * q, bd, idesc, q ? 1u : 0u);
         }
-        mma_commit(smem_u32(&bars.free[b]));
+        mma_commit(smem_u32(&bars.free[i & 3]));
         mma_commit(smem_u32(&bars.full[b]));
+        issued = i;
       }
       if (i < ng) {
-        // given up: wait for the MMAs and the copies still in flight
-        if (i >= 2) mbar_wait(smem_u32(&bars.free[b]), ((i >> 1) & 1) ^ 1, p.status);
-        for (int j = i; j < min(ng, fetched); j += 2)
-          mbar_wait(smem_u32(&bars.weights[j % kStages]), (j / kStages) & 1, p.status);
-        for (int j = i; j < min(ng, fetched_x); j += 2)
+        // given up: wait for the MMAs and the copies that may still be in flight
+        if (issued >= 0) wait_free(issued, nullptr);
+        for (int j = w_from; j < min(ng, w_to); j += 2)
+          mbar_wait(smem_u32(&bars.weights[j % S::kStages]), (j / S::kStages) & 1, p.status);
+        for (int j = x_from; !S::kLoader && j < min(ng, x_to); j += 2)
           mbar_wait(smem_u32(&bars.x[j & 3]), (j >> 2) & 1, p.status);
       }
     }
@@ -269,25 +299,50 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.full[b]), (i >> 1) & 1, p.status, abort));
         if (!ok) break;
         tc_fence_after();
+        const uint32_t from = tmem + lane_off + S::kTmemD + S::kDCols * b + c0;
+        if constexpr (kFp8) {
+          float s4[4];  // of the fragment's rows lane / 4 + 8 j
 #pragma unroll
-        for (int c = 0; c < S::kEpTok; c += kLoad) {
-          uint32_t d[kLoad];
-          tmem_load(tmem + lane_off + kTmemD + S::kDCols * b + c0 + c, d);
-          tmem_wait_ld();
+          for (int j = 0; j < 4; ++j) s4[j] = __shfl_sync(0xffffffffu, s, lane / 4 + 8 * j);
+          const float* sx = sxs + i % kSxStages * kTn + c0 + 2 * (lane & 3);
 #pragma unroll
-          for (int e = 0; e < kLoad; e += 2) {
-            const float v0 = __uint_as_float(d[e]), v1 = __uint_as_float(d[e + 1]);
-            const float* sx = sxs + q * kTn + c0 + c + e;
-            float* to = acc + c + e;
-            if (S::kPacked) {
-              uint64_t v = f32x2(v0, v1);
-              if (kFp8) v = mul_f32x2(v, *reinterpret_cast<const uint64_t*>(sx));
-              const float2 sum = f32x2_split(fma_f32x2(v, f32x2(s, s), f32x2(to[0], to[1])));
-              to[0] = sum.x;
-              to[1] = sum.y;
-            } else {
-              to[0] = fmaf(kFp8 ? v0 * sx[0] : v0, s, to[0]);
-              to[1] = fmaf(kFp8 ? v1 * sx[1] : v1, s, to[1]);
+          for (int c = 0; c < S::kEpTok; c += 16) {
+            const float2 x[2] = {*reinterpret_cast<const float2*>(sx + c), *reinterpret_cast<const float2*>(sx + c + 8)};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // the warp's rows 0 .. 15, then 16 .. 31
+              uint32_t d[8];
+              tmem_ld_frag16(from + c + (static_cast<uint32_t>(16 * half) << 16), d);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const float2 xe = x[e >> 2];
+                const float w = s4[2 * half + (e >> 1 & 1)];
+                float* to = acc + c + 8 * half + e;
+                const uint64_t v = mul_f32x2(f32x2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), f32x2(xe.x, xe.y));
+                const float2 sum = f32x2_split(fma_f32x2(v, f32x2(w, w), f32x2(to[0], to[1])));
+                to[0] = sum.x;
+                to[1] = sum.y;
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < S::kEpTok; c += kLoad) {
+            uint32_t d[kLoad];
+            tmem_load(from + c, d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < kLoad; e += 2) {
+              float* to = acc + c + e;
+              const uint64_t v = f32x2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]));
+              if (S::kPacked) {
+                const float2 sum = f32x2_split(fma_f32x2(v, f32x2(s, s), f32x2(to[0], to[1])));
+                to[0] = sum.x;
+                to[1] = sum.y;
+              } else {
+                to[0] = fmaf(__uint_as_float(d[e]), s, to[0]);
+                to[1] = fmaf(__uint_as_float(d[e + 1]), s, to[1]);
+              }
             }
           }
         }
@@ -298,7 +353,14 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
     }
     // every MMA has completed: the operands and the ring are free for the partial
 #pragma unroll
-    for (int t = 0; t < S::kEpTok; ++t) part[(c0 + t) * S::kLd + r] = acc[t];
+    for (int t = 0; t < S::kEpTok; ++t) {
+      if (!kFp8) {
+        part[(c0 + t) * S::kLd + r] = acc[t];
+      } else {
+        const int e = t & 15, token = c0 + (t & ~15) + (e & 4 ? 8 : 0) + 2 * (lane & 3) + (e & 1);
+        part[token * S::kLd + (warp & 3) * 32 + (e >> 3) * 16 + (e >> 1 & 1) * 8 + (lane >> 2)] = acc[t];
+      }
+    }
   }
   // TMEM goes back before any wait for a peer: kernels on two streams, each waiting in a cluster with TMEM that the
   // other's CTAs need to start, would wait for ever
