@@ -87,7 +87,9 @@ struct W4Params {
   int* status;
   int T, K, groups;
   int tiles0;           // tiles of the first projection: CTA tiles from there on compute the second
-  int split, per;       // CTAs along K, groups per CTA
+  int split, per;       // CTAs of a cluster; groups per CTA (csrc/linear_w4.cu)
+  int share;            // tiles of a cluster (csrc/linear_w4_tc.cu)
+  int all, slices;      // tiles in all, and of the same features (slices of the tokens), there
   bool early;           // the weights may be read before the previous kernel has finished
 
   // Tiles of `rows` features of both projections, in order.
@@ -114,6 +116,31 @@ __device__ __forceinline__ float sum_partials(uint32_t at, int split) {
 #pragma unroll
   for (int q = 1; q < kW4MaxSplit; ++q) sum += v[q];
   return sum;
+}
+// The same of four floats in the CTAs lo .. hi, at `at_hi` in the last one.
+__device__ __forceinline__ float4 sum_partials(uint32_t at, uint32_t at_hi, int lo, int hi) {
+  float4 v[kW4MaxSplit];
+#pragma unroll
+  for (int q = 0; q < kW4MaxSplit; ++q) {
+    v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lo + q <= hi)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[q].x), "=f"(v[q].y), "=f"(v[q].z), "=f"(v[q].w)
+                   : "r"(sm100::mapa(lo + q == hi ? at_hi : at, lo + q))
+                   : "memory");
+  }
+  float4 sum = v[0];
+#pragma unroll
+  for (int q = 1; q < kW4MaxSplit; ++q) {
+    sum.x += v[q].x;
+    sum.y += v[q].y;
+    sum.z += v[q].z;
+    sum.w += v[q].w;
+  }
+  return sum;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return f32_to_bf16_bits(a) | (static_cast<uint32_t>(f32_to_bf16_bits(b)) << 16);
 }
 
 // Eight values of x, as loaded, as MMA operands in the pair order (0,4) (1,5) (2,6) (3,7); E4M3 codes become f16

@@ -258,9 +258,27 @@ def test_linear_parity_large(T, K, N, fp8):
     ok()
 
 
+# More tiles of 128 tokens than fit the GPU at once or than fill it: clusters whose CTAs take parts of several tiles
+# (tails, whole ones and heads), one and two slices of the tokens, K ragged and short.
+@pytest.mark.parametrize("T,K,N", [(130, 8192, 7100), (256, 4160, 7168), (200, 7104, 12900), (100, 5184, 17000),
+                                   (256, 1088, 20001), (65, 256, 60000), (192, 10240, 9600)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_linear_of_shared_tiles(T, K, N, fp8):
+    args = linear_inputs(T, K, N, fp8, T * 131 + K + N)
+    ref, tol = linear_ref(*args)
+    buf = torch.full((T + 2, N), 77.0, dtype=torch.bfloat16, device="cuda")
+    y = run_linear(*args, y=buf[1:T + 1])
+    within(f64(y), ref, tol)
+    assert (buf[0] == 77).all() and (buf[T + 1] == 77).all()
+    again = run_linear(*args)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    ok()
+
+
 @pytest.mark.parametrize("T,K,N0,N1", [(1, 7168, 512, 64), (3, 192, 17, 1), (8, 1088, 1, 700), (5, 128, 9000, 9001),
                                        (32, 1536, 5000, 2600), (16, 192, 50001, 47000), (64, 704, 3000, 5001),
-                                       (100, 1088, 1300, 1301), (256, 64, 8000, 9700)])
+                                       (100, 1088, 1300, 1301), (256, 64, 8000, 9700), (100, 4160, 5000, 9001),
+                                       (140, 4160, 3700, 3601)])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_linear_pair_parity(T, K, N0, N1, fp8):
     """Two projections of one x in one launch, in both kernels; the second one's rows stay its own."""
