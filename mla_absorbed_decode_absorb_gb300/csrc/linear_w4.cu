@@ -296,10 +296,10 @@ cudaError_t launch_rows(const W4Params& p, cudaStream_t stream) {
 cudaError_t launch_linear_w4(W4Params p, cudaStream_t stream) {
   const int slices = (p.T + kTok - 1) / kTok;
   const int64_t tiles = p.tiles(16) * slices;
-  // Warp MMAs pass over the weights once for 8 tokens, the tensor-core kernel once for 16 to 64 but with a longer way
-  // from weight to result: it wins from two passes on once they are over about 36 M weights (1536 x 16384: 17 tokens
-  // 11.2 us against 12.8, 16 tokens 9.9 against 9.5; 16384 x 7168: 16 tokens 26 against 32, 64 tokens 33 against
-  // 94; but 7168 x 576: 64 tokens 9.8 against 7.4, 512 x 512: 7.1 against 2.4).
+  // Warp MMAs pass over the weights once for 8 tokens, the tensor-core kernel once for 16 to 128 but with a longer way
+  // from weight to result: it wins from two passes on once they are over about 36 M weights (us, tensor cores against
+  // warps: 1536 -> 16384, 16 tokens 9.0 against 11.3; 16384 -> 7168, 16 tokens 24 against 28, 64 tokens 28 against 96;
+  // 7168 -> 1536, 32 tokens 8.8 against 8.9, 16 tokens 8.3 against 7.1; 512 -> 512, 256 tokens 5.2 against 3.3).
   if (slices > 1 && (static_cast<int64_t>(p.out[0].N) + p.out[1].N) * p.K * slices > 36000000) return launch_linear_w4_tc(p, stream);
   // Up to one wave of CTAs, 16 rows each and K over all eight warps: the latency of few, short streams counts.
   // Beyond, 32 rows a warp share what it unpacks of x (1536 -> 16384, one token: 6.6 us against 7.4), and fewer warps

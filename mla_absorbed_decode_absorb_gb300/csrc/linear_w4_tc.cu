@@ -503,8 +503,7 @@ cudaError_t launch_tn(W4Params p, cudaStream_t stream) {
   if (S::kShare) {
     // One wave of clusters of `split` CTAs that divide the groups of `share` tiles evenly, whichever leaves a CTA the
     // fewest groups; adding partials up costs about four groups' time (256 tokens, 16384 -> 7168, 112 tiles of 128
-    // groups: 66 us in a CTA each, 62 in clusters of five
-    // for four tiles).
+    // groups: 66 us in a CTA each, 62 in clusters of five for four tiles).
     int64_t best = -1;
     for (int s = 1; s <= kW4MaxSplit; ++s) {
       const int64_t share = (p.all + fit[dev][s] - 1) / fit[dev][s];
@@ -516,7 +515,7 @@ cudaError_t launch_tn(W4Params p, cudaStream_t stream) {
     }
   } else {
     // K over the largest cluster whose CTAs still fit the GPU at once (a second, partial wave costs more) and that
-    // leaves a CTA two groups, or seven where CTAs share an SM (32 tokens, 1536 -> 16384: 10.4 us undivided, 11.7 halved)
+    // leaves a CTA two groups, or seven where CTAs share an SM (32 tokens, 1536 -> 16384: 9.6 us undivided; halved it took 1.3 more)
     for (int s = kW4MaxSplit; s > 1; --s) {
       const int64_t ctas = tiles * s;
       if (ctas > kMaxCtas || p.groups < (ctas <= kMaxCtas / 2 ? 2 : 7) * s || tiles > fit[dev][s]) continue;
