@@ -15,6 +15,10 @@ E4M3 2^-4, fp32 2^-24 relative):
 * cache read back: bf16(fp32(s code)), bit for bit.
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -472,22 +476,22 @@ def chain(ops, x, r, w, w4, scale, out, y8, s, y):
     return y
 
 
+@pytest.mark.parametrize("T,D,N", [(20, 1536, 600), (100, 4160, 9000)])
 @pytest.mark.parametrize("overlap", [0, 1, 2])
-def test_chain_on_a_side_stream_and_replayed(overlap):
+def test_chain_on_a_side_stream_and_replayed(overlap, T, D, N):
     """Norm then projection on a stream of their own, then captured once and replayed on new inputs: the same
     bits as the calls one by one."""
     from mla_absorbed_decode_absorb_gb300 import ops
     before = ops.mla_get_launch_overlap()
     ops.mla_set_launch_overlap(overlap)
     try:
-        T, D, N = 20, 1536, 600
         x, r, w = norm_inputs(T, D, 31)
         x2, r2, _ = norm_inputs(T, D, 32)
         _, _, w4, scale = (t if t is None else t.cuda() for t in linear_inputs(T, D, N, False, 33))
 
         def fresh():
             return (torch.empty_like(x), torch.empty(T, D, dtype=torch.uint8, device="cuda"),
-                    torch.empty(T, 12, dtype=torch.float32, device="cuda"),
+                    torch.empty(T, F.groups(D), dtype=torch.float32, device="cuda"),
                     torch.empty(T, N, dtype=torch.bfloat16, device="cuda"))
 
         ref = [chain(ops, a, b, w, w4, scale, *fresh()).clone() for a, b in ((x, r), (x2, r2))]
@@ -511,6 +515,88 @@ def test_chain_on_a_side_stream_and_replayed(overlap):
         ok()
     finally:
         ops.mla_set_launch_overlap(before)
+
+
+@pytest.mark.parametrize("overlap", [1, 2])
+def test_projections_in_a_row_on_one_buffer(overlap):
+    """y of one projection is x of the next, back to back through both kernels and into a buffer that the call before
+    still reads: each call sees what came before it, eagerly and replayed."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    before = ops.mla_get_launch_overlap()
+    ops.mla_set_launch_overlap(overlap)
+    try:
+        T, D = 96, 4096
+        ws = [[t.cuda() for t in linear_inputs(T, D, D, False, 50 + i)[2:]] for i in range(3)]
+        x0 = linear_inputs(T, D, 64, False, 60)[0].cuda()
+        small = x0[:3].clone()
+
+        def steps(a, b, c, d):
+            for w in ws * 2:
+                ops.mla_linear_w4(a, *w, b)
+                ops.mla_linear_w4(b, *w, a)
+                ops.mla_linear_w4(c, *w, d)
+                ops.mla_linear_w4(d, *w, c)
+
+        def slowly():
+            a, c = x0.clone(), small.clone()
+            for w in ws * 2:
+                for _ in range(2):
+                    a, c = ops.mla_linear_w4(a, *w), ops.mla_linear_w4(c, *w)
+                    torch.cuda.synchronize()
+            return a, c
+
+        ref_a, ref_c = slowly()
+        a, b, c, d = x0.clone(), torch.empty_like(x0), small.clone(), torch.empty_like(small)
+        steps(a, b, c, d)
+        assert torch.equal(a.view(torch.int16), ref_a.view(torch.int16))
+        assert torch.equal(c.view(torch.int16), ref_c.view(torch.int16))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            steps(a, b, c, d)
+        for _ in range(3):
+            a.copy_(x0), c.copy_(small)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(a.view(torch.int16), ref_a.view(torch.int16))
+            assert torch.equal(c.view(torch.int16), ref_c.view(torch.int16))
+        ok()
+    finally:
+        ops.mla_set_launch_overlap(before)
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first use of each kernel is captured: what the library asks the device for then is allowed."""
+    code = """
+import torch
+from mla_absorbed_decode_absorb_gb300 import ops
+g = torch.Generator(device="cuda").manual_seed(0)
+w = torch.randn(9000, 4160, generator=g, device="cuda").to(torch.bfloat16)
+xs = [torch.randn(t, 4160, generator=g, device="cuda").to(torch.bfloat16) for t in (1, 16, 40, 64, 200)]
+gamma = torch.ones(4160, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+
+def calls():
+    w4, s = ops.mla_quantize_w4(w)
+    out = []
+    for x in xs:
+        y8, ys = ops.mla_rms_norm_fp8(x, gamma)
+        out += [ops.mla_linear_w4(x, w4, s), ops.mla_linear_w4_fp8(y8, ys, w4, s)]
+    return out
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, calls()))
+torch.cuda.synchronize()
+assert ops.mla_get_device_status() == ops.MLA_OK
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_calls_at_once():
