@@ -68,9 +68,11 @@ struct TcShape {
   static constexpr int kEpWarps = 4 * (kTn / kEpTok);
   static constexpr int kIssuer = kEpilogue + kEpWarps;         // first of the two warps that issue MMAs
   static constexpr int kACols = kFp8 ? 32 : 64;                // TMEM columns of a group's weights
-  static constexpr int kABufs = kFp8 || kTn > 64 ? 4 : 2;      // ... in place or in use, in front of two accumulators
+  // ... in place or in use, in front of two accumulators: as many as fit (16 tokens, 16384 -> 7168: 23.2 us with three,
+  // 24.1 with two)
+  static constexpr int kABufs = kFp8 || kTn > 64 ? 4 : kTn <= 16 ? 3 : 2;
   static constexpr uint32_t kTmemD = kABufs * kACols;
-  static constexpr int kDCols = kTn <= 64 ? 64 : 128;          // TMEM columns of an accumulator
+  static constexpr int kDCols = kTn <= 16 ? 16 : kTn <= 64 ? 64 : 128;  // TMEM columns of an accumulator
   static constexpr uint32_t kTmemCols = kTn <= 64 ? 256 : 512;
   static constexpr bool kLoader = kTn > 64;                    // x is fetched by a warp of its own
   static constexpr int kThreads = 32 * (kIssuer + 2 + (kLoader ? 1 : 0));
@@ -85,6 +87,7 @@ struct TcShape {
   static constexpr int kSx = kFp8 ? kSxStages * kTn * 4 : 0;   // scales of x
   static constexpr int kSmem = kBody + kMid + kSx + 256 + 1024;
   static_assert(sizeof(Bars) <= 256, "barrier block");
+  static_assert(kTmemD + 2 * kDCols <= kTmemCols, "tensor memory");
   static_assert(kSmem * kPerSm <= 227 * 1024, "shared memory");
 };
 
@@ -198,7 +201,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     bool ok = true;
     for (int i = 0; i < ng; ++i) {
-      const int b = i & (S::kABufs - 1);
+      const int b = i % S::kABufs;
       ok = mbar_wait(smem_u32(&bars.weights[i % kStages]), (i / kStages) & 1, p.status, abort);
       uint32_t w[16];
 #pragma unroll
@@ -301,7 +304,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
         if (i >= 2 && !mbar_wait(smem_u32(&bars.drained[b]), ((i >> 1) & 1) ^ 1, p.status, abort)) break;
         tc_fence_after();
         const uint32_t b0 = smem_u32(smem + (i & 3) * S::kB);
-        const uint32_t d = tmem + S::kTmemD + S::kDCols * b, a0 = tmem + S::kACols * (i & (S::kABufs - 1));
+        const uint32_t d = tmem + S::kTmemD + S::kDCols * b, a0 = tmem + S::kACols * (i % S::kABufs);
 #pragma unroll
         for (int q = 0; q < (kFp8 ? 4 : 8); ++q) {
           const uint64_t bd = smem_desc(b0 + (q >> 2) * S::kBox + (q & 3) * 32, 16, 1024, kSw128);
@@ -514,8 +517,8 @@ cudaError_t launch_tn(W4Params p, cudaStream_t stream) {
       p.share = static_cast<int>(share);
     }
   } else {
-    // K over the largest cluster whose CTAs still fit the GPU at once (a second, partial wave costs more) and that
-    // leaves a CTA two groups, or seven where CTAs share an SM (32 tokens, 1536 -> 16384: 9.6 us undivided; halved it took 1.3 more)
+    // K over the largest cluster whose CTAs still fit the GPU at once (a second, partial wave costs more) and that leaves
+    // a CTA two groups, or seven where CTAs share an SM (32 tokens, 1536 -> 16384: 9.6 us undivided, halved 1.3 more)
     for (int s = kW4MaxSplit; s > 1; --s) {
       const int64_t ctas = tiles * s;
       if (ctas > kMaxCtas || p.groups < (ctas <= kMaxCtas / 2 ? 2 : 7) * s || tiles > fit[dev][s]) continue;
