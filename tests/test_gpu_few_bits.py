@@ -376,6 +376,69 @@ def test_linear_writes_its_rows_only(T, N):
     ok()
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 512, 64), (20, 7168, 2048), (40, 7168, 1536), (100, 8192, 7168), (70, 262144, 3)])
+def test_linear_into_a_row_of_no_alignment(T, K, N):
+    """y two bytes off every larger boundary, at widths that a wider store would take."""
+    args = linear_inputs(T, K, N, False, 22)
+    buf = torch.full((T * N + 8,), 77.0, dtype=torch.bfloat16, device="cuda")
+    y = buf[3:3 + T * N].view(T, N)
+    run_linear(*args, y=y)
+    ref, tol = linear_ref(*args)
+    within(f64(y), ref, tol)
+    assert (buf[:3] == 77).all() and (buf[3 + T * N:] == 77).all()
+    ok()
+
+
+def test_offsets_past_32_bits():
+    """Weights of more than 2^32 values and 2^31 bytes, activations and caches of more than 2^31 elements: rows at the
+    start, on both sides of the borders and at the end."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    N, K = 270000, 16384
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w4 = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda")
+    scale = (torch.rand(N, K // 128, generator=g, device="cuda") / 600 + 1e-3).to(torch.bfloat16)
+    border = 2 ** 31 // (K // 2)
+    rows = torch.tensor([0, 1, 2 ** 31 // K - 1, 2 ** 31 // K, border - 1, border, border + 1, N - 2, N - 1], device="cuda")
+    ref_w = F.weights_w4(w4[rows].cpu().numpy(), f64(scale[rows].cpu()))
+    for T in (2, 12, 100):
+        x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+        y = ops.mla_linear_w4(x, w4, scale)
+        xf = f64(x.cpu())
+        ref, mag = xf @ ref_w.T, np.abs(xf) @ np.abs(ref_w).T
+        within(f64(y[:, rows].cpu()), ref, 2.0 ** -8 * np.abs(ref) + (K + 3 * (K // 128)) * 2.0 ** -23 * mag)
+        del y
+    n = 2 ** 31 // K + 40  # weights of more than 2^31 elements there and back
+    back = ops.mla_dequantize_w4(w4[:n], scale[:n])
+    again, s2 = ops.mla_quantize_w4(back)
+    rows = torch.tensor([0, n - 41, n - 40, n - 1], device="cuda")
+    assert np.array_equal(f64(back[rows].cpu()), F.bf16_round(F.weights_w4(w4[rows].cpu().numpy(), f64(scale[rows].cpu()))))
+    u, s_ref = F.quantize_w4(f64(back[rows].cpu()))
+    assert np.array_equal(again[rows].cpu().numpy(), F.pack_w4(u)) and np.array_equal(f64(s2[rows].cpu()), s_ref)
+    del w4, scale, again, s2
+    # the norm of those rows, in place, and in 8 bits
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    before = back[rows].clone()
+    y8, s8 = ops.mla_rms_norm_fp8(back, w)
+    check_norm(before, None, w, 1e-6, y8=y8[rows], scale=s8[rows])
+    del y8
+    ops.mla_rms_norm(back, w, y=back)
+    check_norm(before, None, w, 1e-6, y=back[rows])
+    del back
+    # a cache read back into more than 2^31 elements: every sequence the same pages
+    B, most = 60, 64 * 1000 + 5
+    c8, sc, kr, pt, _ = fp8_cache([64 * 1001], 6)
+    cache, ptg, _ = to_gpu(c8, sc, kr, pt, np.zeros(1, np.int32))
+    lens = torch.full((B,), most, dtype=torch.int32, device="cuda")
+    rows = ops.mla_read_kv_fp8(cache, ptg.expand(B, -1).contiguous(), lens, most).view(B, 1001 * 64, 576)
+    assert rows.numel() > 2 ** 31
+    assert torch.equal(rows[-1, :most].view(torch.int16), rows[0, :most].view(torch.int16))
+    assert torch.isnan(rows[-1, most:].float()).all()
+    t = most - 1
+    ref = O.f32_to_bf16_bits(O.e4m3_decode(c8[pt[0, t // 64], t % 64]).astype(np.float32) * sc[pt[0, t // 64], t % 64])
+    assert np.array_equal(bits(rows[-1, t, :512]), ref)
+    ok()
+
+
 def test_linear_refusals():
     from mla_absorbed_decode_absorb_gb300 import ops
     x, _, w4, scale = (t if t is None else t.cuda() for t in linear_inputs(4, 256, 8, False, 1))
