@@ -267,11 +267,16 @@ def _arg(t, name: str, dtype, shape, device: int) -> int:
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _new(shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _out(t, name: str, dtype, shape, like):
+    """An output and its address: ``t``, checked as :func:`_arg` does, or a new tensor beside ``like``."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, _device())
 
 
 def _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream):
+    """The call with the addresses of the outputs (or None), which the callers have checked."""
     T, D = shape = x.shape
     dev = _device()
     if x.get_device() != dev:
@@ -289,10 +294,7 @@ def _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream):
         r_out = r if residual_out is None else _arg(residual_out, "residual_out", torch.bfloat16, shape, dev)
     _check("mla_rms_norm", lib.mla_rms_norm(
         x.data_ptr(), x.stride(0) if T > 1 else D, r, r_out, _arg(weight, "weight", torch.bfloat16, (D,), dev), eps,
-        None if y is None else _arg(y, "y", torch.bfloat16, shape, dev),
-        None if y8 is None else _arg(y8, "y8", torch.uint8, shape, dev),
-        None if y_scale is None else _arg(y_scale, "y_scale", torch.float32, (T, _groups(D)), dev),
-        T, D, _stream(stream, dev)))
+        y, y8, y_scale, T, D, _stream(stream, dev)))
 
 
 def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, stream=None):
@@ -300,9 +302,9 @@ def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, 
 
     x [T, D] may have a row stride (a multiple of 8); with ``residual`` the sum h is written to
     ``residual_out`` (default: in place)."""
-    if y is None:
-        y = _new(x.shape, torch.bfloat16, x)
-    _rms_norm(x, weight, eps, residual, residual_out, y, None, None, stream)
+    T, D = shape = x.shape
+    y, y_at = _out(y, "y", torch.bfloat16, shape, x)
+    _rms_norm(x, weight, eps, residual, residual_out, y_at, None, None, stream)
     return y
 
 
@@ -311,25 +313,21 @@ def mla_rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y8=N
     """:func:`mla_rms_norm` with an 8-bit output: (E4M3 codes [T, D] uint8, scales [T, ceil(D/128)] float32),
     what ``mla_linear_w4_fp8`` reads.  With ``y`` the bf16 output is written too."""
     T, D = shape = x.shape
-    if y8 is None:
-        y8 = _new(shape, torch.uint8, x)
-    if y_scale is None:
-        y_scale = _new((T, _groups(D)), torch.float32, x)
-    _rms_norm(x, weight, eps, residual, residual_out, y, y8, y_scale, stream)
+    y8, y8_at = _out(y8, "y8", torch.uint8, shape, x)
+    y_scale, scale_at = _out(y_scale, "y_scale", torch.float32, (T, _groups(D)), x)
+    y_at = None if y is None else _arg(y, "y", torch.bfloat16, shape, _device())
+    _rms_norm(x, weight, eps, residual, residual_out, y_at, y8_at, scale_at, stream)
     return y8, y_scale
 
 
 def mla_quantize_w4(w, w4=None, w_scale=None, stream=None):
     """4-bit weights of ``w [N, K]`` bf16: (half bytes [N, K/2] uint8, scales [N, ceil(K/128)] bf16)."""
     N, K = shape = w.shape
-    dev, codes, scales = _device(), (N, K // 2), (N, _groups(K))
-    if w4 is None:
-        w4 = _new(codes, torch.uint8, w)
-    if w_scale is None:
-        w_scale = _new(scales, torch.bfloat16, w)
+    dev = _device()
+    w4, codes_at = _out(w4, "w4", torch.uint8, (N, K // 2), w)
+    w_scale, scales_at = _out(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), w)
     _check("mla_quantize_w4", lib.mla_quantize_w4(
-        _arg(w, "w", torch.bfloat16, shape, dev), _arg(w4, "w4", torch.uint8, codes, dev),
-        _arg(w_scale, "w_scale", torch.bfloat16, scales, dev), N, K, _stream(stream, dev)))
+        _arg(w, "w", torch.bfloat16, shape, dev), codes_at, scales_at, N, K, _stream(stream, dev)))
     return w4, w_scale
 
 
@@ -337,11 +335,10 @@ def mla_dequantize_w4(w4, w_scale, w=None, stream=None):
     """``w [N, K]`` bf16 of 4-bit weights."""
     N, half = codes = w4.shape
     K, dev = 2 * half, _device()
-    if w is None:
-        w = _new((N, K), torch.bfloat16, w4)
+    w, w_at = _out(w, "w", torch.bfloat16, (N, K), w4)
     _check("mla_dequantize_w4", lib.mla_dequantize_w4(
         _arg(w4, "w4", torch.uint8, codes, dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev),
-        _arg(w, "w", torch.bfloat16, (N, K), dev), N, K, _stream(stream, dev)))
+        w_at, N, K, _stream(stream, dev)))
     return w
 
 
@@ -349,12 +346,10 @@ def mla_linear_w4(x, w4, w_scale, y=None, stream=None):
     """``y [T, N] = x [T, K] w^T`` in bf16 with 4-bit weights (fp32 accumulation, no workspace)."""
     T, K = shape = x.shape
     N, dev = w4.shape[0], _device()
-    if y is None:
-        y = _new((T, N), torch.bfloat16, x)
+    y, y_at = _out(y, "y", torch.bfloat16, (T, N), x)
     _check("mla_linear_w4", lib.mla_linear_w4(
         _arg(x, "x", torch.bfloat16, shape, dev), _arg(w4, "w4", torch.uint8, (N, K // 2), dev),
-        _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev), _arg(y, "y", torch.bfloat16, (T, N), dev),
-        T, K, N, _stream(stream, dev)))
+        _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev), y_at, T, K, N, _stream(stream, dev)))
     return y
 
 
@@ -362,12 +357,11 @@ def mla_linear_w4_fp8(x8, x_scale, w4, w_scale, y=None, stream=None):
     """:func:`mla_linear_w4` of 8-bit activations as :func:`mla_rms_norm_fp8` returns them."""
     T, K = shape = x8.shape
     N, dev, groups = w4.shape[0], _device(), _groups(K)
-    if y is None:
-        y = _new((T, N), torch.bfloat16, x8)
+    y, y_at = _out(y, "y", torch.bfloat16, (T, N), x8)
     _check("mla_linear_w4_fp8", lib.mla_linear_w4_fp8(
         _arg(x8, "x8", torch.uint8, shape, dev), _arg(x_scale, "x_scale", torch.float32, (T, groups), dev),
         _arg(w4, "w4", torch.uint8, (N, K // 2), dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, groups), dev),
-        _arg(y, "y", torch.bfloat16, (T, N), dev), T, K, N, _stream(stream, dev)))
+        y_at, T, K, N, _stream(stream, dev)))
     return y
 
 
@@ -375,12 +369,10 @@ def _w4_pair(x, w0, w1, y0, y1, T, K, dev):
     args, ys = [], []
     for name, (w4, w_scale), y in (("0", w0, y0), ("1", w1, y1)):
         N = w4.shape[0]
-        if y is None:
-            y = _new((T, N), torch.bfloat16, x)
+        y, y_at = _out(y, "y" + name, torch.bfloat16, (T, N), x)
         ys.append(y)
         args += [_arg(w4, "w4_" + name, torch.uint8, (N, K // 2), dev),
-                 _arg(w_scale, "w_scale_" + name, torch.bfloat16, (N, _groups(K)), dev), N,
-                 _arg(y, "y" + name, torch.bfloat16, (T, N), dev)]
+                 _arg(w_scale, "w_scale_" + name, torch.bfloat16, (N, _groups(K)), dev), N, y_at]
     return args, tuple(ys)
 
 
