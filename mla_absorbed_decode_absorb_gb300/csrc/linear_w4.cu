@@ -35,11 +35,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kTok = 8;        // tokens of a CTA: the columns of one MMA
 constexpr int kStages = 4;     // groups a warp has in flight or in use, kM KB each
-constexpr int kOneWave = 456;  // CTAs of 16 rows that are resident at once (152 SMs, three each)
+constexpr int kSms = 152;
 
 // c (+)= a b; with kFirst, c = a b.
 template <bool kF16, bool kFirst>
@@ -73,16 +71,27 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 // kRowWarps warps cover 16 kM rows each, the other kWarps / kRowWarps share their groups of K.
 template <int kRowWarps, int kM>
 struct W4Shape {
+  static constexpr int kThreads = kM == 1 ? 256 : 128;
+  static constexpr int kPerSm = kM == 1 ? 3 : 4;  // CTAs of an SM
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr int kWave = kSms * kPerSm;
   static constexpr int kKWarps = kWarps / kRowWarps;
   static constexpr int kRows = 16 * kM * kRowWarps;
   static constexpr int kLd = kRows + 4;          // floats per token of a partial: conflict-free fragment stores
   static constexpr int kStage = kWarps * kM * 1024;
   static constexpr int kPart = kKWarps * kTok * kLd * 4;  // lies over the ring
   static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
+  // K over a cluster while its CTAs still fit the GPU at once and a warp keeps more than one group (7168 -> 576, one
+  // token: 3.6 us in four, against 4.8 undivided and 3.7 in eight)
+  static int split(int64_t tiles, int groups) {
+    int n = 1;
+    while (kRowWarps == 1 && n < kW4MaxSplit && tiles * n * 2 <= kWave && groups >= 3 * kKWarps * n) n *= 2;
+    return n;
+  }
 };
 
 template <int kRowWarps, int kM, bool kFp8, bool kRagged>
-__global__ void __launch_bounds__(kThreads, kM == 1 ? 3 : 2)
+__global__ void __launch_bounds__(W4Shape<kRowWarps, kM>::kThreads, W4Shape<kRowWarps, kM>::kPerSm)
 linear_w4_kernel(const W4Params p) {
   using S = W4Shape<kRowWarps, kM>;
   using Vec = std::conditional_t<kFp8, uint2, uint4>;  // 8 values of x
@@ -235,7 +244,7 @@ linear_w4_kernel(const W4Params p) {
   const int toks = min(kTok, p.T - t0);
   if (S::kKWarps > 1) {
     // this CTA's K warps in order, into the first one's place
-    for (int e = tid; e < toks * S::kRows; e += kThreads) {
+    for (int e = tid; e < toks * S::kRows; e += S::kThreads) {
       float* at = part + (e / S::kRows) * S::kLd + e % S::kRows;
       float v = at[0];
 #pragma unroll
@@ -248,7 +257,7 @@ linear_w4_kernel(const W4Params p) {
 
   // the cluster's threads share the (token, row) sums, row fastest, each in rank order
   const uint32_t base = smem_u32(part);
-  for (int e = rank * kThreads + tid; e < toks * S::kRows; e += p.split * kThreads) {
+  for (int e = rank * S::kThreads + tid; e < toks * S::kRows; e += p.split * S::kThreads) {
     const int r = e % S::kRows, t = e / S::kRows;
     if (n0 + r >= out.N) continue;
     const float v = sum_partials(base + (t * S::kLd + r) * 4, p.split);
@@ -272,15 +281,10 @@ cudaError_t launch_shape(W4Params p, cudaStream_t stream) {
   const int64_t tiles = p.tiles(S::kRows);
   const int slices = (p.T + kTok - 1) / kTok;
   p.tiles0 = (p.out[0].N + S::kRows - 1) / S::kRows;
-  // K over a cluster while its CTAs still fit the GPU at once and a warp keeps more than one group (7168 -> 576, one
-  // token: 3.6 us in four, against 4.8 undivided and 3.7 in eight)
-  p.split = 1;
-  if (kM == 1)
-    while (p.split < kW4MaxSplit && tiles * slices * p.split * 2 <= kOneWave && 2 * p.groups >= 3 * S::kKWarps * 2 * p.split)
-      p.split *= 2;
+  p.split = S::split(tiles * slices, p.groups);
   p.per = (p.groups + p.split - 1) / p.split;
   p.early = launch_overlap() >= 2;
-  return launch_w4(kernel, dim3(static_cast<unsigned>(tiles) * p.split, 1, slices), kThreads, S::kRing, stream, p.split, p);
+  return launch_w4(kernel, dim3(static_cast<unsigned>(tiles) * p.split, 1, slices), S::kThreads, S::kRing, stream, p.split, p);
 }
 
 template <int kRowWarps, int kM>
@@ -301,13 +305,20 @@ cudaError_t launch_linear_w4(W4Params p, cudaStream_t stream) {
   // warps: 1536 -> 16384, 16 tokens 9.0 against 11.3; 16384 -> 7168, 16 tokens 24 against 28, 64 tokens 28 against 96;
   // 7168 -> 1536, 32 tokens 8.8 against 8.9, 16 tokens 8.3 against 7.1; 512 -> 512, 256 tokens 5.2 against 3.3).
   if (slices > 1 && (static_cast<int64_t>(p.out[0].N) + p.out[1].N) * p.K * slices > 36000000) return launch_linear_w4_tc(p, stream);
-  // Up to one wave of CTAs, 16 rows each and K over all eight warps: the latency of few, short streams counts.
-  // Beyond, 32 rows a warp share what it unpacks of x (1536 -> 16384, one token: 6.6 us against 7.4), and fewer warps
-  // share K where it is short.
-  if (tiles <= kOneWave) return launch_rows<1, 1>(p, stream);
+  // Up to one wave of CTAs, 16 rows each and K over all eight warps: the latency of few, short streams counts; or 32 rows
+  // and four warps where those, divided, fill their wave better (7168 -> 2048, one token: 512 of 608 CTAs 5.4 us, 256 of
+  // 456 6.5).  Beyond, 32 rows a warp share what it unpacks of x (1536 -> 16384, one token: 6.0 us against 7.4), in CTAs
+  // of four warps rather than eight (6.4), and fewer warps share K where it is short.
+  using A = W4Shape<1, 1>;
+  using B = W4Shape<1, 2>;
+  const int64_t tiles2 = p.tiles(32) * slices;
+  if (tiles <= A::kWave) {
+    const int64_t a = tiles * A::split(tiles, p.groups), b = tiles2 * B::split(tiles2, p.groups);
+    return b * A::kWave > a * B::kWave ? launch_rows<1, 2>(p, stream) : launch_rows<1, 1>(p, stream);
+  }
   if (p.groups >= 48) return launch_rows<1, 2>(p, stream);
   if (p.groups >= 4) return launch_rows<2, 2>(p, stream);
-  return launch_rows<8, 2>(p, stream);
+  return launch_rows<4, 2>(p, stream);
 }
 
 }  // namespace mla
