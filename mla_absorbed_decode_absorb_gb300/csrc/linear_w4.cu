@@ -37,7 +37,7 @@ using namespace sm100;
 
 constexpr int kTok = 8;        // tokens of a CTA: the columns of one MMA
 constexpr int kStages = 4;     // groups a warp has in flight or in use, kM KB each
-constexpr int kSms = 152;
+constexpr int kSms = 152;      // of the GPU this is built for: the rules below count in waves of it
 
 // c (+)= a b; with kFirst, c = a b.
 template <bool kF16, bool kFirst>
@@ -82,7 +82,8 @@ struct W4Shape {
   static constexpr int kPart = kKWarps * kTok * kLd * 4;  // lies over the ring
   static constexpr int kRing = kStages * kStage > kPart ? kStages * kStage : kPart;
   // K over a cluster while its CTAs still fit the GPU at once and a warp keeps more than one group (7168 -> 576, one
-  // token: 3.6 us in four, against 4.8 undivided and 3.7 in eight)
+  // token: 3.6 us in four, against 4.8 undivided and 3.7 in eight; in powers of two, because clusters of seven do not
+  // all fit: 16384 -> 1024 9.0 us against 6.9 in four)
   static int split(int64_t tiles, int groups) {
     int n = 1;
     while (kRowWarps == 1 && n < kW4MaxSplit && tiles * n * 2 <= kWave && groups >= 3 * kKWarps * n) n *= 2;

@@ -383,6 +383,7 @@ class LayerSession:
             # laid out once; the bf16 weights are not kept
             for name in ("w_dkv", "w_kr", "w_dq", "w_uq", "w_qr", "w_o"):
                 setattr(self, name, ops.mla_quantize_w4(getattr(self, name), stream=stream))
+            torch.cuda.synchronize(dev)  # a step on another stream, or one that reads weights early, does not wait for them
         # a layer step's input is the hidden state, its result the layer output
         self.step_buffer = self.x
         self.out = self.y
