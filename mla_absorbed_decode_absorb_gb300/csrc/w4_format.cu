@@ -79,14 +79,14 @@ quantize_w4_kernel(const uint16_t* __restrict__ w, uint32_t* __restrict__ w4, ui
       const float rs = __fdividef(1.f, s);
 #pragma unroll
       for (int i = 7; i >= 0; --i)
-        word = word * 16 + __float_as_uint(__fsub_rn(fmaf(x[i], rs, 3072.f), 3072.f) + 12582920.f);
+        word = word * 16 + __float_as_uint(__fsub_rn(fmaf(x[i], rs, 0x1.8p11f), 0x1.8p11f) + 12582920.f);
       word -= 0x4b400000u * 0x11111111u;
     } else {
       // a scale so small that its reciprocal overflows, or itself rounded coarsely: 2^64 times both, and clamped
       const float rs = __fdividef(1.f, s * 0x1p64f);
 #pragma unroll
       for (int i = 7; i >= 0; --i) {
-        const float c = __fsub_rn(fmaf(x[i] * 0x1p64f, rs, 3072.f), 3072.f);
+        const float c = __fsub_rn(fmaf(x[i] * 0x1p64f, rs, 0x1.8p11f), 0x1.8p11f);
         word = word * 16 + (__float_as_uint(fminf(fmaxf(c, -8.f), 7.f) + 12582920.f) & 15u);
       }
     }
