@@ -27,9 +27,10 @@
 // them, so that the work fits the GPU in one even wave: a CTA has the tail of a tile,
 // whole ones, which it stores itself, and the head of another.
 //
-// What bounds it (256 tokens, 16384 -> 7168: 62 us, 0.51 of the measured bf16 rate): the
-// way of a group through unpacking, MMAs and sums; without MMAs, sums and unpacking the
-// same pipeline took 47 us, and leaving out its loads of x or of the weights changed nothing.
+// What bounds it (256 tokens, 16384 -> 7168: 62 us, 0.51 of the measured bf16 rate):
+// unpacking, MMAs and sums take a group about as long each, the unpacking a little
+// longer (undivided tiles 66 us; without the unpacking 58, without most MMAs besides 52,
+// without the sums besides 44); the loads of x and of the weights are not waited for.
 #include "sm100.cuh"
 #include "tmap.cuh"
 #include "w4.cuh"
