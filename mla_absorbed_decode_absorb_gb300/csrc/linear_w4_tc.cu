@@ -530,8 +530,9 @@ cudaError_t launch_tn(W4Params p, cudaStream_t stream) {
   p.early = launch_overlap() >= 2;
   CUtensorMap tm_w[2], tm_x;
   for (int i = 0; i < 2; ++i) {
-    const W4Out& o = p.out[i].N > 0 ? p.out[i] : p.out[0];  // (not read without a second projection)
-    if (!make_tmap_u8_2d(&tm_w[i], o.w4, o.N, p.K / 2, p.K / 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_64B))
+    const W4Out& o = p.out[i];
+    if (o.N == 0) tm_w[i] = tm_w[0];  // no second projection: not read
+    else if (!make_tmap_u8_2d(&tm_w[i], o.w4, o.N, p.K / 2, p.K / 2, 64, kRows, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
   const bool ok = kFp8 ? make_tmap_u8_2d(&tm_x, p.x, p.T, p.K, p.K, kW4Group, kTn, CU_TENSOR_MAP_SWIZZLE_128B)
