@@ -10,6 +10,7 @@ not been built, importing this module raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -112,6 +113,22 @@ def _stream(stream, device=None) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _torch_stream(stream, device=None):
+    """The torch stream of a call's ``stream`` argument: None (the current one), a torch stream or a raw handle."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # torch takes no handle 0 (1: cudaStreamLegacy) for an external stream: it is its own default stream
+    return torch.cuda.default_stream(device) if int(stream) in (0, 1) else torch.cuda.ExternalStream(int(stream), device)
+
+
+def _on(stream):
+    """Where a call allocates and fills what it makes itself: on the stream that it launches on, whose order then
+    holds for the fill, the kernel and the memory's next use alike."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
 
 
 def _dev_or_pinned(t: torch.Tensor, name: str, dtype, shape=None) -> int:
@@ -407,7 +424,8 @@ def mla_read_kv_fp8(cache_fp8, page_table, kv_lens, max_kv_len, rows=None, strea
     slots = page_table.shape[1]
     shape = (B * ((max_kv_len + 63) // 64), 64, D_ROW)
     if rows is None:
-        rows = empty_cache(shape[0], c8.device)
+        with _on(stream):
+            rows = empty_cache(shape[0], c8.device)
     _check("mla_read_kv_fp8", lib.mla_read_kv_fp8(
         _arg(c8, "cache_c8", torch.uint8, (P, 64, D_LATENT), dev),
         _arg(scale, "cache_scale", torch.float32, (P, 64), dev),

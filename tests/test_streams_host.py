@@ -1,0 +1,101 @@
+"""What a call allocates or fills itself belongs to the stream it launches on: checked without a GPU, with the
+library, the streams and the address checks replaced by recorders and every torch operation logged with the
+stream it would have been issued on."""
+
+import contextlib
+import ctypes
+
+import pytest
+import torch
+from torch.utils._python_dispatch import TorchDispatchMode
+
+CURRENT, SIDE = 11, 22  # stream handles
+
+
+class Recorder(TorchDispatchMode):
+    """Logs ("torch", operation, stream), ("launch", function, stream) and waits in the order they happen."""
+
+    def __init__(self):
+        super().__init__()
+        self.stack, self.log = [CURRENT], []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        self.log.append(("torch", func.overloadpacket.__name__, self.stack[-1]))
+        return func(*args, **(kwargs or {}))
+
+    def streams_of(self, *names):
+        return {s for kind, name, s in self.log if kind == "torch" and name in names}
+
+
+class Stream:
+    """A torch stream, as far as the package uses one."""
+
+    rec = None
+
+    def __init__(self, handle, device=None):
+        assert handle not in (0, 1)  # no handle of a stream that ExternalStream can wrap
+        self.handle = self.cuda_stream = handle
+
+    def wait_stream(self, other):
+        self.rec.log.append(("wait", other.handle, self.handle))
+
+    def synchronize(self):
+        self.rec.log.append(("synchronize", "", self.handle))
+
+
+class Lib:
+    """The library: a launch is logged with its last argument, a size query goes to the real one."""
+
+    def __init__(self, rec, real):
+        self.rec, self.real = rec, real
+
+    def __getattr__(self, name):
+        if name.endswith("_size") or name.endswith("_path") or name.endswith("_splits"):
+            return getattr(self.real, name)
+
+        def launch(*args):
+            self.rec.log.append(("launch", name, args[-1]))
+            return 0
+        return launch
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    from mla_absorbed_decode_absorb_gb300 import ops
+    rec = Recorder()
+
+    @contextlib.contextmanager
+    def stream(s):
+        rec.stack.append(s.handle)
+        try:
+            yield
+        finally:
+            rec.stack.pop()
+
+    fake = type("FakeStream", (Stream,), {"rec": rec})
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", fake)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: fake(rec.stack[-1]))
+    monkeypatch.setattr(ops, "lib", Lib(rec, ops.lib))
+    monkeypatch.setattr(ops, "_device", lambda: -1)
+    monkeypatch.setattr(ops, "_dev", lambda t, *a, **k: t.data_ptr())
+    monkeypatch.setattr(ops, "_stream", lambda s, device=None: rec.stack[-1] if s is None else int(s))
+    return rec
+
+
+def fp8_cache(pages):
+    return (torch.zeros(pages, 64, 512, dtype=torch.uint8), torch.zeros(pages, 64),
+            torch.zeros(pages, 64, 64, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("stream,where", [(None, CURRENT), (SIDE, SIDE)])
+def test_read_back_fills_its_rows_on_the_stream_it_reads_on(rec, stream, where):
+    """Filled on the current stream while the read runs on another, the sentinel could land over the rows read back."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    cache, table = fp8_cache(3), torch.zeros(2, 2, dtype=torch.int32)
+    lens = torch.tensor([70, 100], dtype=torch.int32)
+    with rec:
+        rows = ops.mla_read_kv_fp8(cache, table, lens, 100, stream=stream)
+    assert rows.shape == (4, 64, 576) and torch.isnan(rows.float()).all()
+    assert ("launch", "mla_read_kv_fp8", where) in rec.log
+    assert rec.streams_of("full", "fill_", "empty") == {where}
