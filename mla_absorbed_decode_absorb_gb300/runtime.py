@@ -35,6 +35,7 @@ which give the same per-head output ``out``.
 
 from __future__ import annotations
 
+from contextlib import contextmanager
 from dataclasses import dataclass
 
 import torch
@@ -46,6 +47,20 @@ from .workloads import D_LATENT, D_NOPE, D_ROW, N_HEADS, PAGE, Inputs, empty_cac
 # New tokens per sequence from which a step takes the non-absorbed path (the
 # switch point the MLA pages give for prefill / chunked prefill).
 PREFILL_MIN_NEW_TOKENS = 64
+
+
+@contextmanager
+def _laid_out_on(stream, device):
+    """A session's constructor, all on one stream: the fills, copies and kernels of ``stream`` (None: the current one)
+    follow one another and what the current stream held, memory that is given back meanwhile is not taken for
+    something else by work that does not wait for it, and the session is in place when its constructor returns, for
+    steps on any stream."""
+    main, current = ops._torch_stream(stream, device), torch.cuda.current_stream(device)
+    if stream is not None:
+        main.wait_stream(current)
+    with torch.cuda.stream(main):
+        yield
+    main.synchronize()
 
 
 class StepGraph:
@@ -93,9 +108,13 @@ class DecodeSession:
         self.path = path
         # append + absorb_q as one launch (both on the caller's stream)
         self.fused_prologue = bool(fused_prologue) and path == "absorbed" and not self.overlap_append
+        with _laid_out_on(stream, self.device):
+            self._lay_out(inp)
+
+    def _lay_out(self, inp):
         dev = self.device
         self.max_kv_len = int(inp.kv_lens.max()) if self.B else self.n_q
-        self.rope = ops.rope_table(self.max_kv_len + 1, dev, stream)
+        self.rope = ops.rope_table(self.max_kv_len + 1, dev)
         self.w_uk = inp.w_uk.to(dev)
         self.w_uv = inp.w_uv.to(dev)
         self.page_table = inp.page_table.to(dev)
@@ -116,10 +135,10 @@ class DecodeSession:
                 continue
             if self.cache_format == "fp8":
                 ops.mla_append_kv_fp8(hc.to(dev)[None], hk.to(dev)[None], zero, self.page_table[b:b + 1],
-                                      self.rope, self.cache_fp8, stream=stream)
+                                      self.rope, self.cache_fp8)
             else:
                 ops.mla_append_kv(hc.to(dev)[None], hk.to(dev)[None], zero, self.page_table[b:b + 1], self.rope,
-                                  self.cache, stream=stream)
+                                  self.cache)
         self.lse = torch.empty(self.B, self.n_q, N_HEADS, dtype=torch.float32, device=dev)
         self.out = torch.empty(self.B, self.n_q, N_HEADS, D_NOPE, dtype=torch.bfloat16, device=dev)
         if self.path == "absorbed":
@@ -176,11 +195,7 @@ class DecodeSession:
         ops.mla_copy(host_out, self.out, stream)
 
     def _main(self, stream):
-        if stream is None:
-            return torch.cuda.current_stream(self.device)
-        if isinstance(stream, torch.cuda.Stream):
-            return stream
-        return torch.cuda.ExternalStream(int(stream), device=self.device)
+        return ops._torch_stream(stream, self.device)
 
     # individual stages (the bench times them one by one)
     def append(self, stream=None):

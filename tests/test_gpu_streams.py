@@ -32,3 +32,31 @@ def test_read_back_on_another_stream_while_the_current_one_is_busy():
         assert same_bits(rows, ref) and same_bits(first, ref.cpu())
     assert np.isnan(ref.view(4, -1)[2].float().cpu().numpy()).all()
     ok()
+
+
+@pytest.mark.parametrize("n_q,cache_format", [(70, "fp8"), (70, "bf16"), (2, "bf16"), (2, "fp8")])
+def test_a_session_laid_out_on_a_busy_stream(n_q, cache_format, monkeypatch):
+    """A session whose constructor's stream has work in front of it and between the pools' fills, stepped on yet
+    another stream at once: the bits of a session of the current stream.  Sequences of one length, whose histories
+    are copied into the same memory one after the other."""
+    from mla_absorbed_decode_absorb_gb300 import runtime
+    from mla_absorbed_decode_absorb_gb300 import workloads as W
+    inp = W.generate(W.custom("busy", [130, 130, 130, 0], n_q=n_q, cache_format=cache_format), seed=8)
+    s = runtime.DecodeSession(inp)
+    s.step()
+    torch.cuda.synchronize()
+    real = runtime.empty_cache
+
+    def slow_empty_cache(*args):
+        torch.cuda._sleep(BUSY)
+        return real(*args)
+
+    monkeypatch.setattr(runtime, "empty_cache", slow_empty_cache)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(a):
+        torch.cuda._sleep(BUSY)
+    t = runtime.DecodeSession(inp, stream=a)
+    t.step(b)
+    b.synchronize()
+    assert same_bits(t.out, s.out) and same_bits(t.lse, s.lse)
+    ok()

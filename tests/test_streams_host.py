@@ -99,3 +99,28 @@ def test_read_back_fills_its_rows_on_the_stream_it_reads_on(rec, stream, where):
     assert rows.shape == (4, 64, 576) and torch.isnan(rows.float()).all()
     assert ("launch", "mla_read_kv_fp8", where) in rec.log
     assert rec.streams_of("full", "fill_", "empty") == {where}
+
+
+def one_stream(rec, where):
+    """Everything in the log ran on ``where``, behind what the current stream held, and was waited for at the end."""
+    kinds = [k for k, _, _ in rec.log]
+    assert {s for k, _, s in rec.log if k in ("torch", "launch")} == {where}
+    if where != CURRENT:
+        assert rec.log[0] == ("wait", CURRENT, where)
+    assert rec.log[-1] == ("synchronize", "", where)
+    assert "launch" in kinds
+
+
+@pytest.mark.parametrize("stream,where", [(None, CURRENT), (SIDE, SIDE)])
+@pytest.mark.parametrize("n_q,cache_format", [(70, "fp8"), (70, "bf16"), (2, "bf16"), (2, "fp8")])
+def test_a_decode_session_is_laid_out_on_one_stream(rec, stream, where, n_q, cache_format):
+    """The pools' fills, the history's copies, the appends and the page table of the rows read back: on two streams the
+    appends would not wait for the fills, a step could read a table that is not written yet, and the memory of one
+    sequence's history could be taken for the next one's while the append still reads it."""
+    from mla_absorbed_decode_absorb_gb300 import workloads as W
+    from mla_absorbed_decode_absorb_gb300.runtime import DecodeSession
+    inp = W.generate(W.custom("streams", [0, 63, 130], n_q=n_q, cache_format=cache_format), seed=3)
+    with rec:
+        s = DecodeSession(inp, device="cpu", stream=stream)
+    assert s.path == ("non_absorbed" if n_q == 70 else "absorbed")
+    one_stream(rec, where)
