@@ -366,10 +366,13 @@ class LayerSession:
         self.li = li
         self.fold = bool(fold)
         self.weights, self.activations = weights, activations
-        dev = torch.device(device)
-        self.device = dev
-        self.dec = DecodeSession(li.base, device=dev, split_pages=split_pages, stream=stream)
-        d = self.dec
+        self.device = torch.device(device)
+        with _laid_out_on(stream, self.device):
+            self._lay_out(li, split_pages, norms, residual)
+
+    def _lay_out(self, li, split_pages, norms, residual):
+        dev = self.device
+        self.dec = d = DecodeSession(li.base, device=dev, split_pages=split_pages)
         self.T = d.B * d.n_q
         self.d_model = li.workload.d_model
         self.x = li.x.to(dev).reshape(self.T, self.d_model)
@@ -394,18 +397,17 @@ class LayerSession:
         need = max(need, ops.mla_linear_pair_workspace_size(self.T, self.d_model, self.w_dkv.shape[0],
                                                             self.w_kr.shape[0]))
         self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        if weights == "w4":
+        if self.weights == "w4":
             # laid out once; the bf16 weights are not kept
             for name in ("w_dkv", "w_kr", "w_dq", "w_uq", "w_qr", "w_o"):
-                setattr(self, name, ops.mla_quantize_w4(getattr(self, name), stream=stream))
-            torch.cuda.synchronize(dev)  # a step on another stream, or one that reads weights early, does not wait for them
+                setattr(self, name, ops.mla_quantize_w4(getattr(self, name)))
         # a layer step's input is the hidden state, its result the layer output
         self.step_buffer = self.x
         self.out = self.y
         if self.fold:
-            self._prepare_folds(stream)
+            self._prepare_folds()
 
-    def _prepare_folds(self, stream=None):
+    def _prepare_folds(self):
         """W_QK[(h, m), c] = sum_d W_UK[h, d, m] W_UQ[h*128 + d, c] and
         W_OV[j, (h, m)] = sum_d W_O[j, h*128 + d] W_UV[h, d, m], each by mla_linear calls
         (K = d_h = 128; row blocks of at most 256)."""
@@ -421,13 +423,12 @@ class LayerSession:
             uk_t = d.w_uk[h].t().contiguous()                          # [512, 128]
             uq_t = self.w_uq[h * dh:(h + 1) * dh].t().contiguous()      # [1536, 128]
             for r0 in range(0, dc, 256):
-                ops.mla_linear(uk_t[r0:r0 + 256], uq_t, self.w_qk[h * dc + r0:h * dc + r0 + 256], ws, stream)
+                ops.mla_linear(uk_t[r0:r0 + 256], uq_t, self.w_qk[h * dc + r0:h * dc + r0 + 256], ws)
             o_blk = self.w_o[:, h * dh:(h + 1) * dh].contiguous()       # [d_model, 128]
             uv_t = d.w_uv[h].t().contiguous()                           # [512, 128]
             for r0 in range(0, self.d_model, 256):
                 rows = min(256, self.d_model - r0)
-                ops.mla_linear_strided(o_blk[r0:r0 + rows], uv_t, self.w_ov[r0:, h * dc:], H * dc, dc, dc, ws,
-                                       stream)
+                ops.mla_linear_strided(o_blk[r0:r0 + rows], uv_t, self.w_ov[r0:, h * dc:], H * dc, dc, dc, ws)
         self.o_lat_bf16 = torch.empty(self.T, H * dc, dtype=torch.bfloat16, device=dev)
         need = max(ops.mla_linear_workspace_size(self.T, dq, H * dc),
                    ops.mla_linear_workspace_size(self.T, H * dc, self.d_model))

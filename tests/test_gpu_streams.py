@@ -60,3 +60,23 @@ def test_a_session_laid_out_on_a_busy_stream(n_q, cache_format, monkeypatch):
     b.synchronize()
     assert same_bits(t.out, s.out) and same_bits(t.lse, s.lse)
     ok()
+
+
+@pytest.mark.parametrize("kind", ["fold", "few_bits"])
+def test_a_layer_laid_out_on_a_busy_stream(kind):
+    """Folded and quantised weights, whose inputs are given back while the constructor's stream is still busy."""
+    from mla_absorbed_decode_absorb_gb300 import runtime
+    from mla_absorbed_decode_absorb_gb300 import workloads as W
+    li = W.generate_layer(W.Workload("busy", batch=2, n_q=2, lengths=(5, 130), d_model=1024), seed=9)
+    kw = {"fold": dict(fold=True), "few_bits": dict(weights="w4")}[kind]
+    s = runtime.LayerSession(li, **kw)
+    s.step()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(a):
+        torch.cuda._sleep(BUSY)
+    t = runtime.LayerSession(li, stream=a, **kw)
+    t.step(b)
+    b.synchronize()
+    assert same_bits(t.y, s.y)
+    ok()

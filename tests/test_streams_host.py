@@ -3,7 +3,6 @@ library, the streams and the address checks replaced by recorders and every torc
 stream it would have been issued on."""
 
 import contextlib
-import ctypes
 
 import pytest
 import torch
@@ -77,6 +76,8 @@ def rec(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", fake)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: fake(rec.stack[-1]))
     monkeypatch.setattr(ops, "lib", Lib(rec, ops.lib))
+    monkeypatch.setattr(ops, "mla_linear_strided", lambda *a, stream=None: rec.log.append(  # asks its y for a CUDA tensor
+        ("launch", "mla_linear_strided", rec.stack[-1] if len(a) < 8 or a[7] is None else int(a[7]))))
     monkeypatch.setattr(ops, "_device", lambda: -1)
     monkeypatch.setattr(ops, "_dev", lambda t, *a, **k: t.data_ptr())
     monkeypatch.setattr(ops, "_stream", lambda s, device=None: rec.stack[-1] if s is None else int(s))
@@ -124,3 +125,29 @@ def test_a_decode_session_is_laid_out_on_one_stream(rec, stream, where, n_q, cac
         s = DecodeSession(inp, device="cpu", stream=stream)
     assert s.path == ("non_absorbed" if n_q == 70 else "absorbed")
     one_stream(rec, where)
+
+
+@pytest.mark.parametrize("stream,where", [(None, CURRENT), (SIDE, SIDE)])
+@pytest.mark.parametrize("kind", ["plain", "fold", "few_bits"])
+def test_a_layer_session_is_laid_out_on_one_stream(rec, stream, where, kind):
+    """... and its weights: quantised or folded from tensors that are given back while the launches still read them."""
+    from mla_absorbed_decode_absorb_gb300 import workloads as W
+    from mla_absorbed_decode_absorb_gb300.runtime import LayerNorms, LayerSession
+    li = W.generate_layer(W.Workload("streams", batch=2, n_q=2, lengths=(0, 70), d_model=256), seed=3)
+    kw = {"plain": {}, "fold": dict(fold=True)}.get(kind)
+    if kw is None:
+        ones = [torch.ones(n, dtype=torch.bfloat16) for n in (256, W.D_Q_LATENT, W.D_LATENT)]
+        kw = dict(weights="w4", activations="fp8", norms=LayerNorms(*ones), residual=li.x.clone())
+    with rec:
+        LayerSession(li, device="cpu", stream=stream, **kw)
+    one_stream(rec, where)
+
+
+def test_raw_handles_of_streams(monkeypatch):
+    """A handle is an external stream; 0 and 1 (the legacy default stream), which torch does not take for one, are its
+    default stream."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    assert ops._torch_stream(SIDE) == ("external", SIDE)
+    assert ops._torch_stream(0) == ops._torch_stream(1) == "default"
