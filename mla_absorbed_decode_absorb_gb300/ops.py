@@ -4,7 +4,9 @@ Argument marshalling only: every function checks dtypes, devices and
 contiguity, passes raw device pointers and the current CUDA stream to the
 C entry point of the same name, and raises :class:`MLAError` on a non-OK
 status.  Outputs not supplied by the caller are allocated with torch (the
-library itself never allocates).  There is no fallback: if the library has
+library itself never allocates), on the stream that the call launches on:
+a call with ``stream=s`` makes what the same call inside
+``torch.cuda.stream(s)`` would.  There is no fallback: if the library has
 not been built, importing this module raises.
 """
 
@@ -131,6 +133,27 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
 
 
+def _kept(t, stream):
+    """What a call made on ``stream`` and returns: the memory also waits for the current stream, on which the caller
+    goes on, before it is used again."""
+    if stream is not None and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _empty(shape, dtype, device, stream):
+    """A workspace, on the stream of the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(shape, dtype, device, stream):
+    """An output, on the stream of the call."""
+    return _kept(_empty(shape, dtype, device, stream), stream)
+
+
 def _dev_or_pinned(t: torch.Tensor, name: str, dtype, shape=None) -> int:
     """An output the kernels may store to across the host link: a CUDA tensor, or a
     pinned (page-locked) host tensor."""
@@ -163,7 +186,7 @@ def mla_abi_version() -> int:
 
 def rope_table(max_positions: int, device=None, stream=None) -> torch.Tensor:
     """[max_positions, 64] float32: cos then sin of the 32 RoPE frequencies (mla_rope_table_init)."""
-    t = torch.empty(max_positions, D_ROPE, dtype=torch.float32, device=device or "cuda")
+    t = _new((max_positions, D_ROPE), torch.float32, device or "cuda", stream)
     _check("mla_rope_table_init", lib.mla_rope_table_init(t.data_ptr(), int(max_positions), _stream(stream)))
     return t
 
@@ -215,12 +238,12 @@ def mla_linear_pair(x, w0, w1, y0=None, y1=None, workspace=None, stream=None):
     T, K = x.shape
     N0, N1 = w0.shape[0], w1.shape[0]
     if y0 is None:
-        y0 = torch.empty(T, N0, dtype=torch.bfloat16, device=x.device)
+        y0 = _new((T, N0), torch.bfloat16, x.device, stream)
     if y1 is None:
-        y1 = torch.empty(T, N1, dtype=torch.bfloat16, device=x.device)
+        y1 = _new((T, N1), torch.bfloat16, x.device, stream)
     need = mla_linear_pair_workspace_size(T, K, N0, N1)
     if need and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream)
     _check("mla_linear_pair", lib.mla_linear_pair(
         _dev(x, "x", torch.bfloat16, (T, K)), int(T), int(K),
         _dev(w0, "w0", torch.bfloat16, (N0, K)), int(N0), _dev(y0, "y0", torch.bfloat16, (T, N0)),
@@ -235,10 +258,10 @@ def mla_linear(x, w, y=None, workspace=None, stream=None):
     T, K = x.shape
     N = w.shape[0]
     if y is None:
-        y = torch.empty(T, N, dtype=torch.bfloat16, device=x.device)
+        y = _new((T, N), torch.bfloat16, x.device, stream)
     need = mla_linear_workspace_size(T, K, N)
     if need and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream)
     _check("mla_linear", lib.mla_linear(
         _dev(x, "x", torch.bfloat16, (T, K)), _dev(w, "w", torch.bfloat16, (N, K)),
         _dev(y, "y", torch.bfloat16, (T, N)), int(T), int(K), int(N),
@@ -253,7 +276,7 @@ def mla_linear_strided(x, w, y, y_ld, seg, seg_ld, workspace=None, stream=None):
     N = w.shape[0]
     need = mla_linear_workspace_size(T, K, N)
     if need and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream)
     if y.dtype != torch.bfloat16 or not y.is_cuda:
         raise TypeError("y must be a CUDA bf16 tensor")
     extent = y.untyped_storage().nbytes() // y.element_size() - y.storage_offset()
@@ -284,10 +307,11 @@ def _arg(t, name: str, dtype, shape, device: int) -> int:
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _out(t, name: str, dtype, shape, like):
+def _out(t, name: str, dtype, shape, like, stream):
     """An output and its address: ``t``, checked as :func:`_arg` does, or a new tensor beside ``like``."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = torch.empty(shape, dtype=dtype, device=like.device) if stream is None else \
+            _new(shape, dtype, like.device, stream)
         return t, t.data_ptr()
     return t, _arg(t, name, dtype, shape, _device())
 
@@ -320,7 +344,7 @@ def mla_rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, 
     x [T, D] may have a row stride (a multiple of 8); with ``residual`` the sum h is written to
     ``residual_out`` (default: in place)."""
     T, D = shape = x.shape
-    y, y_at = _out(y, "y", torch.bfloat16, shape, x)
+    y, y_at = _out(y, "y", torch.bfloat16, shape, x, stream)
     _rms_norm(x, weight, eps, residual, residual_out, y_at, None, None, stream)
     return y
 
@@ -330,8 +354,8 @@ def mla_rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, y8=N
     """:func:`mla_rms_norm` with an 8-bit output: (E4M3 codes [T, D] uint8, scales [T, ceil(D/128)] float32),
     what ``mla_linear_w4_fp8`` reads.  With ``y`` the bf16 output is written too."""
     T, D = shape = x.shape
-    y8, y8_at = _out(y8, "y8", torch.uint8, shape, x)
-    y_scale, scale_at = _out(y_scale, "y_scale", torch.float32, (T, _groups(D)), x)
+    y8, y8_at = _out(y8, "y8", torch.uint8, shape, x, stream)
+    y_scale, scale_at = _out(y_scale, "y_scale", torch.float32, (T, _groups(D)), x, stream)
     y_at = None if y is None else _arg(y, "y", torch.bfloat16, shape, _device())
     _rms_norm(x, weight, eps, residual, residual_out, y_at, y8_at, scale_at, stream)
     return y8, y_scale
@@ -341,8 +365,8 @@ def mla_quantize_w4(w, w4=None, w_scale=None, stream=None):
     """4-bit weights of ``w [N, K]`` bf16: (half bytes [N, K/2] uint8, scales [N, ceil(K/128)] bf16)."""
     N, K = shape = w.shape
     dev = _device()
-    w4, codes_at = _out(w4, "w4", torch.uint8, (N, K // 2), w)
-    w_scale, scales_at = _out(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), w)
+    w4, codes_at = _out(w4, "w4", torch.uint8, (N, K // 2), w, stream)
+    w_scale, scales_at = _out(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), w, stream)
     _check("mla_quantize_w4", lib.mla_quantize_w4(
         _arg(w, "w", torch.bfloat16, shape, dev), codes_at, scales_at, N, K, _stream(stream, dev)))
     return w4, w_scale
@@ -352,7 +376,7 @@ def mla_dequantize_w4(w4, w_scale, w=None, stream=None):
     """``w [N, K]`` bf16 of 4-bit weights."""
     N, half = codes = w4.shape
     K, dev = 2 * half, _device()
-    w, w_at = _out(w, "w", torch.bfloat16, (N, K), w4)
+    w, w_at = _out(w, "w", torch.bfloat16, (N, K), w4, stream)
     _check("mla_dequantize_w4", lib.mla_dequantize_w4(
         _arg(w4, "w4", torch.uint8, codes, dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev),
         w_at, N, K, _stream(stream, dev)))
@@ -363,7 +387,7 @@ def mla_linear_w4(x, w4, w_scale, y=None, stream=None):
     """``y [T, N] = x [T, K] w^T`` in bf16 with 4-bit weights (fp32 accumulation, no workspace)."""
     T, K = shape = x.shape
     N, dev = w4.shape[0], _device()
-    y, y_at = _out(y, "y", torch.bfloat16, (T, N), x)
+    y, y_at = _out(y, "y", torch.bfloat16, (T, N), x, stream)
     _check("mla_linear_w4", lib.mla_linear_w4(
         _arg(x, "x", torch.bfloat16, shape, dev), _arg(w4, "w4", torch.uint8, (N, K // 2), dev),
         _arg(w_scale, "w_scale", torch.bfloat16, (N, _groups(K)), dev), y_at, T, K, N, _stream(stream, dev)))
@@ -374,7 +398,7 @@ def mla_linear_w4_fp8(x8, x_scale, w4, w_scale, y=None, stream=None):
     """:func:`mla_linear_w4` of 8-bit activations as :func:`mla_rms_norm_fp8` returns them."""
     T, K = shape = x8.shape
     N, dev, groups = w4.shape[0], _device(), _groups(K)
-    y, y_at = _out(y, "y", torch.bfloat16, (T, N), x8)
+    y, y_at = _out(y, "y", torch.bfloat16, (T, N), x8, stream)
     _check("mla_linear_w4_fp8", lib.mla_linear_w4_fp8(
         _arg(x8, "x8", torch.uint8, shape, dev), _arg(x_scale, "x_scale", torch.float32, (T, groups), dev),
         _arg(w4, "w4", torch.uint8, (N, K // 2), dev), _arg(w_scale, "w_scale", torch.bfloat16, (N, groups), dev),
@@ -382,11 +406,11 @@ def mla_linear_w4_fp8(x8, x_scale, w4, w_scale, y=None, stream=None):
     return y
 
 
-def _w4_pair(x, w0, w1, y0, y1, T, K, dev):
+def _w4_pair(x, w0, w1, y0, y1, T, K, dev, stream):
     args, ys = [], []
     for name, (w4, w_scale), y in (("0", w0, y0), ("1", w1, y1)):
         N = w4.shape[0]
-        y, y_at = _out(y, "y" + name, torch.bfloat16, (T, N), x)
+        y, y_at = _out(y, "y" + name, torch.bfloat16, (T, N), x, stream)
         ys.append(y)
         args += [_arg(w4, "w4_" + name, torch.uint8, (N, K // 2), dev),
                  _arg(w_scale, "w_scale_" + name, torch.bfloat16, (N, _groups(K)), dev), N, y_at]
@@ -397,7 +421,7 @@ def mla_linear_w4_pair(x, w0, w1, y0=None, y1=None, stream=None):
     """``y0 = x w0^T`` and ``y1 = x w1^T`` in one launch, each weight a (w4, w_scale) pair."""
     T, K = shape = x.shape
     dev = _device()
-    args, ys = _w4_pair(x, w0, w1, y0, y1, T, K, dev)
+    args, ys = _w4_pair(x, w0, w1, y0, y1, T, K, dev, stream)
     _check("mla_linear_w4_pair", lib.mla_linear_w4_pair(
         _arg(x, "x", torch.bfloat16, shape, dev), T, K, *args, _stream(stream, dev)))
     return ys
@@ -407,7 +431,7 @@ def mla_linear_w4_fp8_pair(x8, x_scale, w0, w1, y0=None, y1=None, stream=None):
     """:func:`mla_linear_w4_pair` of 8-bit activations as :func:`mla_rms_norm_fp8` returns them."""
     T, K = shape = x8.shape
     dev = _device()
-    args, ys = _w4_pair(x8, w0, w1, y0, y1, T, K, dev)
+    args, ys = _w4_pair(x8, w0, w1, y0, y1, T, K, dev, stream)
     _check("mla_linear_w4_fp8_pair", lib.mla_linear_w4_fp8_pair(
         _arg(x8, "x8", torch.uint8, shape, dev), _arg(x_scale, "x_scale", torch.float32, (T, _groups(K)), dev), T, K,
         *args, _stream(stream, dev)))
@@ -426,6 +450,7 @@ def mla_read_kv_fp8(cache_fp8, page_table, kv_lens, max_kv_len, rows=None, strea
     if rows is None:
         with _on(stream):
             rows = empty_cache(shape[0], c8.device)
+        _kept(rows, stream)
     _check("mla_read_kv_fp8", lib.mla_read_kv_fp8(
         _arg(c8, "cache_c8", torch.uint8, (P, 64, D_LATENT), dev),
         _arg(scale, "cache_scale", torch.float32, (P, 64), dev),
@@ -507,7 +532,7 @@ def mla_decode_attn_fp8_partial(q_abs, cache_fp8, page_table, kv_lens, n_q, max_
 def mla_absorb_q(q_nope, q_rope, seq_lens_before, w_uk, rope, q_abs=None, stream=None):
     B, n_q = q_nope.shape[:2]
     if q_abs is None:
-        q_abs = torch.empty(B, n_q, N_HEADS, D_ROW, dtype=torch.bfloat16, device=q_nope.device)
+        q_abs = _new((B, n_q, N_HEADS, D_ROW), torch.bfloat16, q_nope.device, stream)
     _check("mla_absorb_q", lib.mla_absorb_q(
         _dev(q_nope, "q_nope", torch.bfloat16, (B, n_q, N_HEADS, D_NOPE)),
         _dev(q_rope, "q_rope", torch.bfloat16, (B, n_q, N_HEADS, D_ROPE)),
@@ -632,11 +657,12 @@ def mla_decode_attn(q_abs, cache, page_table, kv_lens, n_q, max_kv_len, split_pa
     """Split attention plus combine; returns (o_latent [B,n_q,128,512] f32, lse [B,n_q,128] f32 or None)."""
     B = kv_lens.shape[0]
     if o_latent is None:
-        o_latent = torch.empty(B, n_q, N_HEADS, D_LATENT, dtype=torch.float32, device=q_abs.device)
+        o_latent = _new((B, n_q, N_HEADS, D_LATENT), torch.float32, q_abs.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty(B, n_q, N_HEADS, dtype=torch.float32, device=q_abs.device)
+        lse = _new((B, n_q, N_HEADS), torch.float32, q_abs.device, stream)
     if workspace is None:
-        workspace = alloc_workspace(B, n_q, max_kv_len, split_pages, q_abs.device)
+        with _on(stream):
+            workspace = alloc_workspace(B, n_q, max_kv_len, split_pages, q_abs.device)
     _check("mla_decode_attn", lib.mla_decode_attn(*_decode_args(
         q_abs, cache, page_table, kv_lens, n_q, max_kv_len, split_pages, workspace, o_latent, lse, stream)))
     return o_latent, lse
@@ -661,7 +687,7 @@ def mla_decode_combine(B, n_q, max_kv_len, split_pages, workspace, o_latent, lse
 def mla_out_absorb(o_latent, w_uv, out=None, stream=None):
     B, n_q = o_latent.shape[:2]
     if out is None:
-        out = torch.empty(B, n_q, N_HEADS, D_NOPE, dtype=torch.bfloat16, device=o_latent.device)
+        out = _new((B, n_q, N_HEADS, D_NOPE), torch.bfloat16, o_latent.device, stream)
     _check("mla_out_absorb", lib.mla_out_absorb(
         _dev(o_latent, "o_latent", torch.float32, (B, n_q, N_HEADS, D_LATENT)),
         _dev(w_uv, "w_uv", torch.bfloat16, (N_HEADS, D_NOPE, D_LATENT)),
@@ -674,7 +700,7 @@ def mla_combine_out_absorb(B, n_q, max_kv_len, split_pages, workspace, o_latent,
                            stream=None):
     """Split merge + value up-projection in one launch (the merged O' is not written)."""
     if out is None:
-        out = torch.empty(B, n_q, N_HEADS, D_NOPE, dtype=torch.bfloat16, device=w_uv.device)
+        out = _new((B, n_q, N_HEADS, D_NOPE), torch.bfloat16, w_uv.device, stream)
     _check("mla_combine_out_absorb", lib.mla_combine_out_absorb(
         int(B), int(n_q), int(max_kv_len), int(split_pages),
         0 if workspace is None else _dev(workspace, "workspace", torch.uint8),
@@ -692,9 +718,9 @@ def mla_decompress_kv(cache, page_table, kv_lens, max_kv_len, w_uk, w_uv, k_nope
     B = int(kv_lens.shape[0])
     shape = (B, N_HEADS, int(max_kv_len), D_NOPE)
     if k_nope is None:
-        k_nope = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        k_nope = _new(shape, torch.bfloat16, cache.device, stream)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        v = _new(shape, torch.bfloat16, cache.device, stream)
     _check("mla_decompress_kv", lib.mla_decompress_kv(
         _dev(cache, "cache", torch.bfloat16), int(cache.shape[0]),
         _dev(page_table, "page_table", torch.int32), int(page_table.shape[1]),
@@ -711,7 +737,7 @@ def mla_prefill_attn(q_nope, q_rope, seq_lens_before, rope, k_nope, v, cache, pa
     B, n_q = q_nope.shape[:2]
     max_kv_len = int(k_nope.shape[2])
     if out is None:
-        out = torch.empty(B, n_q, N_HEADS, D_NOPE, dtype=torch.bfloat16, device=q_nope.device)
+        out = _new((B, n_q, N_HEADS, D_NOPE), torch.bfloat16, q_nope.device, stream)
     _check("mla_prefill_attn", lib.mla_prefill_attn(
         _dev(q_nope, "q_nope", torch.bfloat16, (B, n_q, N_HEADS, D_NOPE)),
         _dev(q_rope, "q_rope", torch.bfloat16, (B, n_q, N_HEADS, D_ROPE)),

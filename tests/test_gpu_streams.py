@@ -80,3 +80,33 @@ def test_a_layer_laid_out_on_a_busy_stream(kind):
     b.synchronize()
     assert same_bits(t.y, s.y)
     ok()
+
+
+def test_outputs_of_another_stream_share_no_memory_with_pending_work():
+    """An output made on a side stream: not in memory whose last use on the current stream is still to come, neither
+    what the current stream gave back before the call nor an earlier output that it still reads."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, K, N = 8, 1024, 4096
+    w4, scale = ops.mla_quantize_w4(torch.randn(N, K, generator=g, device="cuda").to(torch.bfloat16))
+    x1, x2 = (torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    ref1, ref2 = ops.mla_linear_w4(x1, w4, scale), ops.mla_linear_w4(x2, w4, scale)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        scratch = torch.empty_like(ref1)
+        torch.cuda._sleep(BUSY)
+        scratch.fill_(7.0)
+        del scratch  # given back, but written later
+        y = ops.mla_linear_w4(x1, w4, scale, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert same_bits(y, ref1)
+        torch.cuda._sleep(BUSY)
+        later = y.clone()
+        del y  # given back, but read later
+        y = ops.mla_linear_w4(x2, w4, scale, stream=side)
+        torch.cuda.synchronize()
+        assert same_bits(later, ref1) and same_bits(y, ref2)
+        del y, later
+    ok()

@@ -80,6 +80,7 @@ def rec(monkeypatch):
         ("launch", "mla_linear_strided", rec.stack[-1] if len(a) < 8 or a[7] is None else int(a[7]))))
     monkeypatch.setattr(ops, "_device", lambda: -1)
     monkeypatch.setattr(ops, "_dev", lambda t, *a, **k: t.data_ptr())
+    monkeypatch.setattr(ops, "_dev_or_pinned", lambda t, *a, **k: t.data_ptr())
     monkeypatch.setattr(ops, "_stream", lambda s, device=None: rec.stack[-1] if s is None else int(s))
     return rec
 
@@ -151,3 +152,51 @@ def test_raw_handles_of_streams(monkeypatch):
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
     assert ops._torch_stream(SIDE) == ("external", SIDE)
     assert ops._torch_stream(0) == ops._torch_stream(1) == "default"
+
+
+def calls():
+    """Every call that makes an output or a workspace when it is given none: (name, arguments)."""
+    bf, i32 = torch.bfloat16, torch.int32
+
+    def z(*shape, dtype=bf):
+        return torch.zeros(*shape, dtype=dtype)
+    T, K, N = 3, 4096, 64  # K split: the bf16 projections take a workspace
+    w4 = (z(N, K // 2, dtype=torch.uint8), z(N, K // 128))
+    lens, table, cache = z(1, dtype=i32), z(1, 2, dtype=i32), z(2, 64, 576)
+    heads, rope = z(128, 128, 512), z(8, 64, dtype=torch.float32)
+    q, qr, prior = z(1, 1, 128, 128), z(1, 1, 128, 64), z(1, dtype=i32)
+    q_abs, o = z(1, 1, 128, 576), z(1, 1, 128, 512, dtype=torch.float32)
+    kv = z(1, 128, 100, 128)
+    x8, sx = z(T, K, dtype=torch.uint8), z(T, K // 128, dtype=torch.float32)
+    return [
+        ("mla_rms_norm", (z(T, K), z(K))), ("mla_rms_norm_fp8", (z(T, K), z(K))),
+        ("mla_quantize_w4", (z(N, K),)), ("mla_dequantize_w4", w4),
+        ("mla_linear_w4", (z(T, K), *w4)), ("mla_linear_w4_fp8", (x8, sx, *w4)),
+        ("mla_linear_w4_pair", (z(T, K), w4, w4)), ("mla_linear_w4_fp8_pair", (x8, sx, w4, w4)),
+        ("mla_read_kv_fp8", (fp8_cache(2), table, lens, 100)),
+        ("rope_table", (8, "cpu")), ("mla_linear", (z(T, K), z(N, K))),
+        ("mla_linear_pair", (z(T, K), z(N, K), z(N, K))),
+        ("mla_absorb_q", (q, qr, prior, heads, rope)),
+        ("mla_decode_attn", (q_abs, cache, table, lens, 1, 100)),
+        ("mla_out_absorb", (o, heads)),
+        ("mla_combine_out_absorb", (1, 1, 100, 0, z(16, dtype=torch.uint8), None, heads)),
+        ("mla_decompress_kv", (cache, table, lens, 100, heads, heads)),
+        ("mla_prefill_attn", (q, qr, prior, rope, kv, kv, cache, table, lens)),
+    ]
+
+
+@pytest.mark.parametrize("stream,where", [(None, CURRENT), (SIDE, SIDE)])
+@pytest.mark.parametrize("name,args", [pytest.param(*c, id=c[0]) for c in calls()])
+def test_what_a_call_makes_belongs_to_its_stream(rec, monkeypatch, stream, where, name, args):
+    """Memory taken on the current stream may have been given back there by work that is still running, and its next
+    user there does not wait for the launch.  What the caller gets is held for the current stream too."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    held = []
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: held.append((t.data_ptr(), s.handle)))
+    with rec:
+        out = getattr(ops, name)(*args, stream=stream)
+    assert rec.log[-1][::2] == ("launch", where)
+    assert rec.streams_of("empty", "empty_strided", "empty_like", "full") == {where}
+    made = [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+    assert sorted(held) == ([] if stream is None else sorted((t.data_ptr(), CURRENT) for t in made))
