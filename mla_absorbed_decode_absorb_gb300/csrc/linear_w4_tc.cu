@@ -282,8 +282,9 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
         fetch_x(i, x_at);
         advance(x_at, 2);
       };
+      // behind the early fetches, and in front of the first bounded wait: its time must not count the previous kernel's
+      if (p.early) grid_dep_wait();
       if (!S::kLoader) {
-        if (p.early) grid_dep_wait();
         fetch_x_here(b);
         fetch_x_here(b + 2);
       }
