@@ -65,15 +65,20 @@ def _laid_out_on(stream, device):
 
 class StepGraph:
     """A session's step captured once into a CUDA graph (the session's buffers are
-    fixed, so every replay runs the same kernels on the current step inputs)."""
+    fixed, so every replay runs the same kernels on the current step inputs).  The
+    warm-up steps in front of the capture leave a layer's residual as it was."""
 
     def __init__(self, session, warmup: int = 2):
         self.session = session
         self.stream = torch.cuda.Stream(device=session.device)
         self.stream.wait_stream(torch.cuda.current_stream(session.device))
+        residual = getattr(session, "residual", None)  # all that a step adds to
         with torch.cuda.stream(self.stream):
+            before = None if residual is None else residual.clone()
             for _ in range(warmup):  # lazy one-time setup (attributes, tables) outside the capture
                 session.step(self.stream)
+            if residual is not None:
+                residual.copy_(before)
         torch.cuda.current_stream(session.device).wait_stream(self.stream)
         torch.cuda.synchronize(session.device)
         self.graph = torch.cuda.CUDAGraph()
@@ -524,7 +529,7 @@ class LayerSession:
         return head + self.dec.stage_names() + ["proj_out"]
 
     def capture(self, warmup: int = 2) -> "StepGraph":
-        """The layer's step as one CUDA graph.  With ``residual``, the warm-up steps and every replay add to it."""
+        """The layer's step as one CUDA graph.  With ``residual``, every replay adds to it; the capture does not."""
         return StepGraph(self, warmup)
 
     def __getattr__(self, name):
