@@ -319,6 +319,22 @@ class LayerNorms:
     eps: float = 1e-6
 
 
+def _check_residual(residual, elements, device):
+    """What LayerSession's ``residual`` has to be."""
+    if residual.dtype != torch.bfloat16:
+        raise TypeError(f"residual must be torch.bfloat16, got {residual.dtype}")
+    if residual.numel() != elements:
+        raise ValueError(f"residual must have {elements} elements, got {residual.numel()}")
+    there = residual.device
+    if there.type == device.type:
+        if there.type == "cuda" and there.index != (torch.cuda.current_device() if device.index is None else device.index):
+            raise ValueError(f"residual is on {there}, another device than the session's")
+        if not residual.is_contiguous():
+            raise ValueError("residual is added to in place: it must be contiguous")
+    elif there.type != "cpu":
+        raise ValueError(f"residual is on {there}, neither the session's device nor the host")
+
+
 class LayerSession:
     """One MLA decode layer from the hidden state, as in the pages' decode listing
     ("DeepSeek MLA 架构详解", forward_decode), on top of a :class:`DecodeSession`:
@@ -345,8 +361,10 @@ class LayerSession:
 
     With ``norms`` (:class:`LayerNorms`) the step begins with ``norm_in``: the hidden
     state is normed (``mla_rms_norm``), and c^Q and c^KV are normed behind their
-    projections.  With ``residual`` [B, n_q, d_model] besides, ``norm_in`` first adds
-    the hidden state to it, in place (the residual stream).
+    projections.  With ``residual`` [B, n_q, d_model] bf16 besides, ``norm_in`` first
+    adds the hidden state to it, in place (the residual stream): a contiguous tensor of
+    the session's device is that memory itself, which several layers may share; a host
+    tensor is copied, and ``self.residual`` is the copy.
 
     ``weights="w4"`` holds the six projections in 4 bits with group scales
     (``mla_quantize_w4`` once, ``mla_linear_w4`` a step: 0.52 bytes a weight instead of
@@ -368,6 +386,8 @@ class LayerSession:
             raise ValueError("8-bit activations come from the norms and go to 4-bit weights")
         if residual is not None and norms is None:
             raise ValueError("the residual is added before the norm of the hidden state")
+        if residual is not None:
+            _check_residual(residual, li.workload.batch * li.workload.n_q * li.workload.d_model, torch.device(device))
         self.li = li
         self.fold = bool(fold)
         self.weights, self.activations = weights, activations

@@ -39,3 +39,28 @@ def test_a_capture_leaves_the_residual_as_it_was(kw):
             torch.cuda.synchronize()
             assert same_bits(t.residual, res) and same_bits(t.y, y)
     assert ops.mla_get_device_status() == ops.MLA_OK
+
+
+def test_whose_memory_the_residual_is():
+    """A tensor of the device is added to in place and may be shared by layers; a host tensor, dense or not, is copied
+    and stays as it is."""
+    from mla_absorbed_decode_absorb_gb300.runtime import LayerSession
+    li = W.generate_layer(SMALL["mtp"], seed=22)
+    n, r = norms(li, 3), residual_of(li)
+    shared = r.cuda()
+    layers = [LayerSession(li, norms=n, residual=shared) for _ in range(2)]
+    assert all(s.residual.data_ptr() == shared.data_ptr() for s in layers)
+    strided = r.reshape(-1, li.workload.d_model).t().contiguous().t()
+    assert not strided.is_contiguous()
+    for host in (r, strided):
+        before = host.clone()
+        own = LayerSession(li, norms=n, residual=host)
+        own.step()
+        torch.cuda.synchronize()
+        once = (li.x.float() + r.float()).to(torch.bfloat16).cuda()
+        assert same_bits(own.residual.view(once.shape), once) and torch.equal(host.float(), before.float())
+    for s in layers:
+        s.step()
+    own.step()
+    torch.cuda.synchronize()
+    assert same_bits(shared.view(own.residual.shape), own.residual)
