@@ -491,7 +491,8 @@ mla_status mla_rms_norm(const mla_bf16* x, int64_t x_ld, const mla_bf16* residua
  *
  * mla_quantize_w4 -- that form of w [N, K] bf16 (finite): s = bf16(max|w| / 7),
  *   or 1 where that is zero; u = clamp(round(w / s), -8, 7) + 8, nearest even.
- *   IEEE operations throughout: the same codes on every run.
+ *   The codes and scales are those of exact arithmetic (no quotient is so near a tie that
+ *   the kernel's roundings could decide it), the same on every run.
  * mla_dequantize_w4 -- w [N, K] bf16 out: bf16((u - 8) * s).
  * mla_linear_w4 -- y[t][n] = bf16(sum_k x[t][k] (u[n][k] - 8) s[n][k / 128]): mla_linear
  *   with such weights.  x [T, K] bf16, y [T, N] bf16 out, 1 <= T <= MLA_LINEAR_MAX_T.

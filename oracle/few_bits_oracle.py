@@ -45,9 +45,10 @@ def norm_scale(v):
 
 
 def bf16_round(v: np.ndarray) -> np.ndarray:
-    """The nearest bf16 value, ties to even, of finite values in bf16's normal range."""
-    m, e = np.frexp(np.asarray(v, np.float64))
-    return np.ldexp(np.rint(np.ldexp(m, 8)), e - 8)
+    """The nearest bf16 value, ties to even, of finite values below bf16's overflow (below 2^-126 the step is 2^-133)."""
+    v = np.asarray(v, np.float64)
+    step = np.maximum(np.frexp(v)[1], -125) - 8
+    return np.ldexp(np.rint(np.ldexp(v, -step)), step)
 
 
 def quantize_w4(w):
