@@ -503,9 +503,11 @@ mla_status mla_rms_norm(const mla_bf16* x, int64_t x_ld, const mla_bf16* residua
  *   fewer where few tokens leave the projections latency-bound (K may be split
  *   differently from two calls, which only reorders the float32 sums).
  * The products u - 8 times x are exact and summed in float32, the scales are
- * applied to each group's sum in float32, and y is rounded once.  K is split
- * over the CTAs of a cluster, whose partials are added in a fixed order on
- * chip: no workspace, and a result that does not depend on timing.
+ * applied to each group's sum in float32, and y is rounded once.  A group's sum of
+ * (u - 8) x and its product with s have to lie in float32's range; the scales may
+ * take all of theirs.  K is split over the CTAs of a cluster, whose partials are
+ * added in a fixed order on chip: no workspace, and a result that does not depend
+ * on timing.
  * 1 <= N <= MLA_W4_MAX_N, K a multiple of 64, 64 .. MLA_W4_MAX_K, and N * ceil(K / 128)
  * below 2^31 (MLA_ERR_UNSUPPORTED beyond); an output must not overlap an input or the other.
  */

@@ -363,7 +363,7 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
         for (int q = 0; q < 4; ++q) {
           if (j0 + q >= n) break;
           const int i = (S::kShare ? from_group : 0) + j0 + q, b = i & 1;
-          const float s = bf16_bits_to_f32(next[q]) * (kFp8 ? 512.f : 1.f);  // E4M3 weights carry 2^-9
+          const float s = bf16_bits_to_f32(next[q]);
           next[q] = j0 + q + 4 < n ? sw[j0 + q + 4] : uint16_t(0);
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.full[b]), (i >> 1) & 1, p.status, abort));
           if (!ok) break;
@@ -416,6 +416,12 @@ linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_cons
         }
       }
       if (!ok) break;
+      // E4M3 weights carry 2^-9.  It is taken off the sums here, not off the scales in front of them: those go up to
+      // 2^125, and 2^9 times that is no fp32 value.
+      if (kFp8) {
+#pragma unroll
+        for (int t = 0; t < S::kEpTok; ++t) acc[t] *= 512.f;
+      }
       asm volatile("" : "+r"(from_group));  // found again rather than kept in registers: the loop has none to spare
       const At at = at_group(from_group);
       const W4Out out = at.second ? p.out[1] : p.out[0];
