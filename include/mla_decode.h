@@ -463,7 +463,8 @@ mla_status mla_prefill_attn(const mla_bf16* q_nope, const mla_bf16* q_rope, cons
  *   y = bf16(v)
  *   y_scale[t, g] = s = max(max|v| / 448, 2^-100) over columns [128 g, 128 g + 128)
  *   y8 = E4M3(v / s), nearest even
- * h, its sum of squares and v are float32 (h is not rounded before the norm).
+ * h, its sum of squares and v are float32 (h is not rounded before the norm); a quotient
+ * within float32's rounding of halfway between two codes may go to either.
  *   x            [T, D] bf16, row t at x + t * x_ld (x_ld >= D, a multiple of 8)
  *   residual     [T, D] bf16 (nullable, with residual_out)
  *   residual_out [T, D] bf16 out; may be `residual` itself
