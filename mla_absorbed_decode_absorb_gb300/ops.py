@@ -102,16 +102,19 @@ def _check(where: str, status: int) -> None:
         raise MLAError(where, status)
 
 
-_device = torch._C._cuda_getDevice  # the current device, on which the kernels run
+# The current device, on which the kernels run, and a device's current stream: torch's own shortcuts to them (a call's
+# checks take as long as a small launch), or, in a torch that lacks them, the public functions.
+_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream(stream, device=None) -> int:
     if stream is None:
-        # the raw handle of torch.cuda.current_stream(), without building its Python object
         if device is None:
             torch.cuda.init()
             device = _device()
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _current_raw_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
