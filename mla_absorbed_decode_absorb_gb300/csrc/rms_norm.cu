@@ -165,8 +165,8 @@ cudaError_t launch_shape(const NormParams& p, cudaStream_t stream) {
   const int chunks = p.D >> 3;
   const int rows = kSpan == 32 ? kThreads / 32 : 1;
   const int threads = kSpan == 32 ? kThreads : ((chunks + kChunks - 1) / kChunks + 31) / 32 * 32;
-  return launch_kernel(rms_norm_kernel<kChunks, kThreads, kSpan>, dim3((p.T + rows - 1) / rows), dim3(threads), 0,
-                       stream, p);
+  const unsigned ctas = (static_cast<unsigned>(p.T) + rows - 1) / rows;  // T + rows - 1 may be no int
+  return launch_kernel(rms_norm_kernel<kChunks, kThreads, kSpan>, dim3(ctas), dim3(threads), 0, stream, p);
 }
 
 }  // namespace
