@@ -590,9 +590,10 @@ mla_status mla_copy_async(void* dst, const void* src, size_t bytes, cudaStream_t
  *      the same ordering guarantees as 0.
  *   2  as 1, and the weight matrices w_uk (mla_absorb_q), w_uv
  *      (mla_out_absorb, mla_combine_out_absorb) and w4 with w_scale (the
- *      mla_linear_w4 calls) are read BEFORE the previous kernel has completed.  Only valid while no work still running on the
- *      stream writes those weights (fixed inference weights).  Likewise
- *      mla_copy_async reads a host-memory source before that point.
+ *      mla_linear_w4 calls) are read BEFORE the previous kernel has completed.
+ *      Only valid while no work still running on the stream writes those weights
+ *      (fixed inference weights).  Likewise mla_copy_async reads a host-memory
+ *      source before that point.
  *
  * The level is process-wide and read at each launch.  MLA_ERR_INVALID_ARG for a
  * level outside 0..2.  A launch whose predecessor on the stream is not a kernel

@@ -15,22 +15,25 @@
 // The scales of 8-bit x are one for each token, i.e. for each column of the accumulator.
 // Read as rows (a lane a row) every lane needs every token's, which filled the port of
 // shared memory; read in the warp MMA's fragment layout a lane needs a quarter of them
-// (256 tokens, 16384 -> 7168: 82 us against 93).
+// (256 tokens, 16384 -> 7168: 75 us; with rows it was 11 more).
 //
 // Up to 64 tokens two such CTAs share an SM (256 TMEM columns each) and hide each
 // other's waits.  Beyond, one has the SM: four operand buffers in front of the
-// accumulators and a warp that only fetches x (256 tokens, 16384 -> 7168: 68 us; with
-// x fetched by the issuers 72, with two operand buffers as well 81).
+// accumulators and a warp that only fetches x (256 tokens, 16384 -> 7168: 62 us; with
+// x fetched by the issuers it was 4 more, with two operand buffers as well 13).  The tile
+// of 64 tokens of 8-bit x has more sums and scales than registers and spills 108 bytes.
 //
 // K is split over a cluster, whose partials meet in distributed shared memory in rank
 // order.  Beyond 64 tokens a cluster's CTAs divide the groups of several tiles among
 // them, so that the work fits the GPU in one even wave: a CTA has the tail of a tile,
 // whole ones, which it stores itself, and the head of another.
 //
-// What bounds it (256 tokens, 16384 -> 7168: 62 us, 0.51 of the measured bf16 rate):
-// unpacking, MMAs and sums take a group about as long each, the unpacking a little
-// longer (undivided tiles 66 us; without the unpacking 58, without most MMAs besides 52,
-// without the sums besides 44); the loads of x and of the weights are not waited for.
+// What bounds it (256 tokens, 16384 -> 7168: 62 us, 0.51 of the measured bf16 rate): no
+// unit (issue slots 51 %, ALU 47 %, tensor pipe 45 % busy), nor the loads of x and of the
+// weights, which are not waited for.  Of 66 us in undivided tiles 44 are left without the
+// unpacking (58 without it alone), most MMAs (64.8) and the sums (63.8): two thirds are
+// the way of a group through the waits from weights to ready, issue, commit and back,
+// 0.35 us of it, whose links have not been measured apart.
 #include "sm100.cuh"
 #include "tmap.cuh"
 #include "w4.cuh"

@@ -14,14 +14,18 @@ namespace mla {
 constexpr int kW4Group = MLA_W4_GROUP;
 __host__ __device__ inline int w4_groups(int K) { return (K + kW4Group - 1) / kW4Group; }
 
-// (v & mask) | bits as the one instruction it is (left to itself the compiler made two, and this conversion is what
-// bounds a projection of few tokens).
+// (v & mask) | bits as the one instruction it is (left to itself the compiler made two, and this conversion is most of
+// what a projection of few tokens issues).
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
   uint32_t d;
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
   return d;
 }
 
+// Integers to floats without a conversion instruction, by the published method of placing them in the low bits of a
+// constant's significand and taking the constant off (Kim, Henry, Fahim, Hassan Awadalla: "Who Says Elephants Can't
+// Run: Bringing Large Scale MoE Models into Cloud Scale Production", 2022); the constants follow from the formats.
+//
 // The eight half bytes u_0 .. u_7 of a word as four bf16 pairs (u_i - 8, u_{i+4} - 8),
 // i = 0 .. 3: 0x4300 is 128, whose bf16 unit in the last place is 1, so 0x4300 | u
 // is 128 + u, and the difference to 136 is exact.
@@ -32,7 +36,6 @@ __device__ __forceinline__ void w4_pairs(uint32_t v, uint32_t (&p)[4]) {
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(biased), "r"(0x43084308u));
   }
 }
-
 
 // The eight half bytes in their own order, as pairs (u_{2i} - 8, u_{2i+1} - 8): two instructions more.
 __device__ __forceinline__ void w4_pairs_natural(uint32_t v, uint32_t (&p)[4]) {
