@@ -83,8 +83,9 @@ constexpr int kOffP = kOffR + kChunk;       // P: a chunk for each page, or for 
 constexpr int kOffBar = kOffP + 2 * kChunk;
 constexpr int kOffHx = kOffBar + 320;  // a row's four maxima, then its four sums; double buffered
 constexpr int kOffScale = kOffX + 2 * kBufs<true> * kHalf<true>;  // FP8: scales of a tile's tokens, double buffered
+constexpr int kOffLog2 = kOffScale + 2 * 4 * 2 * kPage;  // and, of each softmax warp's 32, their exponents
 constexpr int kSmemBytes = kOffHx + 2 * 4 * 4 * kRows;
-static_assert(2 * kBufs<false> * kHalf<false> == 16 * kChunk && kOffScale + 2 * 4 * 2 * kPage <= kOffR, "buffers");
+static_assert(2 * kBufs<false> * kHalf<false> == 16 * kChunk && kOffLog2 + 4 * kSoftThreads <= kOffR, "buffers");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemO = 0;    // O': column 128 h + c of lane l is latent column 256 (l / 64) + 128 h + c
 constexpr uint32_t kTmemS = 256;  // two score buffers of 64 columns
@@ -516,6 +517,7 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     float* hx = reinterpret_cast<float*>(smem + kOffHx) + r;  // the row's slots, 64 apart
     const int slot = quarter * kRows;
     const float4* sc = reinterpret_cast<const float4*>(smem + kOffScale) + 8 * quarter;
+    float* logs = reinterpret_cast<float*>(smem + kOffLog2) + 32 * warp;  // (the warp's 32 tokens are the same in all its rows)
     const uint32_t s_free = mapa(smem_u32(&bars.s_free[0]), 0), p_full = mapa(smem_u32(&bars.p_full[0]), 0);
     float score_log2 = kScaleLog2;  // a score's factor, in exponents of 2
     float m = -INFINITY, l = 0.f;
@@ -590,7 +592,6 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const uint64_t word = there ? view_bits(v, view_page(v, k0 + 2 * i + hf)) : 0ull;
       const uint32_t w = static_cast<uint32_t>(word >> (32 * ch));
       float2 st[16];  // FP8: the tokens' scales
-      float up_log2 = 0.f;
       if (kFp8) {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.sc_full[buf]), (i >> 1) & 1, p.status, abort)) && ok;
 #pragma unroll
@@ -606,10 +607,9 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (!(w >> (2 * c + 1) & 1u)) st[c].y = 0.f;
           }
         }
-        float top = 0.f;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) top = fmaxf(top, fmaxf(st[c].x, st[c].y));
-        up_log2 = log2f(top);  // -inf where this thread sees nothing
+        // log2 of the scales, a lane's token each (one nobody sees: its score is -inf, whatever its scale)
+        logs[lane] = (w >> lane & 1u) != 0 ? log2f(reinterpret_cast<const float*>(sc)[buf * 2 * kPage + lane]) : 0.f;
+        __syncwarp();
       }
       ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&bars.s_full[buf]), (i >> 1) & 1, p.status, abort)) && ok;
       tc_fence_after();
@@ -646,14 +646,26 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (!(w >> c & 1u)) sv[c] = -INFINITY;
       }
       float m8[8];
+      if (kFp8) {
+        // of weight times scale, token by token: a large scale under a low score must not lift it (a bound of
+        // the largest score plus the largest scale did, and pushed every real weight out of E4M3's range)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) m8[c] = fmaxf(fmaxf(sv[c], sv[c + 8]), fmaxf(sv[c + 16], sv[c + 24]));
+        for (int c = 0; c < 8; ++c) {
+          const float4 f = reinterpret_cast<const float4*>(logs)[c];
+          const float2 x = f32x2_split(fma_f32x2(f32x2(sv[4 * c], sv[4 * c + 1]), scale2, f32x2(f.x, f.y)));
+          const float2 y = f32x2_split(fma_f32x2(f32x2(sv[4 * c + 2], sv[4 * c + 3]), scale2, f32x2(f.z, f.w)));
+          m8[c] = fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y));
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m8[c] = fmaxf(fmaxf(sv[c], sv[c + 8]), fmaxf(sv[c + 16], sv[c + 24]));
+      }
       const float top = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                               fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
       // The row's maximum over its four threads, in exponents of 2; FP8: of weight times scale, which is
-      // what P holds (an upper bound of it).  The slots are written again behind the next tile's barrier.
+      // what P holds.  The slots are written again behind the next tile's barrier.
       float* hb = hx + buf * 4 * kRows;
-      hb[slot] = top * score_log2 + up_log2;
+      hb[slot] = kFp8 ? top : top * score_log2;
       ok = named_barrier_and(1, kSoftThreads, ok);  // the warps leave together
       if (!ok) break;
       const float mx = fmaxf(fmaxf(hb[0], hb[kRows]), fmaxf(hb[2 * kRows], hb[3 * kRows]));

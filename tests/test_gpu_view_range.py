@@ -1,0 +1,63 @@
+"""Attention over the FP8 cache where a row's weights, its tokens' scales or its query's two parts span many powers of two,
+against the plain float64 definition on the values that the cache stands for.
+
+Tolerances.  A weight times its token's scale is rounded to 8 bits (half a step, 2^-8 of it, uniform at the worst:
+2^-8 / sqrt(3) = 2.3e-3 rms), and the output likewise: 3.2e-3, and the repository's 5e-3 for a head by itself, relative
+L2 of its O' and of its outputs."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import view_oracle as V
+from test_gpu_view import PAGE, Problem, clean_status, f64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [0, 1, 37, 63, 64, 90, 127]
+
+
+def fill(p, b, c, k, scale=None):
+    """Sequence b's latent values c [T, 512] and rotated keys k [T, 64] into the FP8 cache, and what it then stands for."""
+    s = c.abs().amax(1) / 448.0 if scale is None else scale
+    code, key = (c / s[:, None]).to(torch.float8_e4m3fn), (k / s[:, None]).to(torch.float16)
+    t = torch.arange(len(c))
+    at = (p.table[b, t // PAGE].long(), t % PAGE)
+    p.parts[0][at], p.parts[1][at], p.parts[2][at] = code.view(torch.uint8), s, key
+    p.rows[b] = torch.cat([code.double() * s.double()[:, None], key.double() * s.double()[:, None]], 1).numpy()
+
+
+def check(p, window=0, lse_tol=1.5e-3):
+    """Each head's O' (one split) and outputs (one, and more), relative to the head's own norm."""
+    seen = [V.visible(L, p.n_q, window) for L in p.prior]
+    w = f64(p.w_uv)[HEADS]
+    for split in (1 << 20, 3):
+        out, lse, latent = p.run(split, window)
+        for b in range(p.B):
+            o_ref, lse_ref = V.attend(f64(p.q[b])[:, HEADS], p.rows[b], seen[b])
+            assert np.abs(f64(lse[b])[:, HEADS] - lse_ref).max() < lse_tol
+            ref = np.einsum("nhm,hdm->nhd", o_ref, w)
+            err = np.linalg.norm(f64(out[b])[:, HEADS] - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+            assert err.max() < 5e-3, (split, err)
+            if p.splits == 1:
+                err = np.linalg.norm(f64(latent[b])[:, HEADS] - o_ref, axis=-1) / np.linalg.norm(o_ref, axis=-1)
+                assert err.max() < 5e-3, err
+
+
+@pytest.mark.parametrize("shift", [0, 7, 9, 13, 16])
+def test_large_scales_with_low_scores(shift):
+    """Tokens whose scale is 2^shift times the others' and whose score is 37 nats lower weigh nothing, and take nothing
+    from the others' weights."""
+    p = Problem([200, 70], 2, seed=shift, fp8=True)
+    g = torch.Generator().manual_seed(shift)
+    for b in range(p.B):
+        n = p.prior[b] + p.n_q
+        c, k = torch.randn(n, 512, generator=g), torch.randn(n, 64, generator=g)
+        c[:, 511], k[:, 0] = 0.0, 0.0
+        s = c.abs().amax(1) / 448.0
+        far = torch.arange(n) % 7 == 3
+        c[far], k[far], s[far] = 0.0, 0.0, 2.0 ** (shift - 7)
+        c[far, 511], k[far, 0] = 448.0 * 2.0 ** (shift - 7), -64.0
+        fill(p, b, c, k, s)
+    p.q[..., 511], p.q[..., 512] = 0.0, 8.0  # 8 x -64 / sqrt(192) = -37
+    check(p)
