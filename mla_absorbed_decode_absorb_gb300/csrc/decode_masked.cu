@@ -32,11 +32,14 @@
 // buffer, needed last), the query (72 KB) and P (16 KB) fill the shared memory.
 //
 // The FP8 cache keeps this shape and multiplies the E4M3 codes as they are (kind::f8f6f4,
-// K = 32 at the same time as K = 16 of 16 bits), with the other operand in two E4M3 parts:
-// 8 significant bits, as bf16 has.  x = x1 + x2 with x1 = E4M3(x) and x2 = E4M3(x - x1):
-// a bf16 query splits without loss (its rows scaled by a power of two, down to 2^-10 of the
-// row's largest value), and P to 2^-8 of a weight at the worst, 2^-16 of the row's largest
-// absolutely.  Codes take half the bytes of bf16 rows on the way and in shared memory, so three
+// K = 32 at the same time as K = 16 of 16 bits), with the other operand in two 8-bit parts.
+// The query: x1 = E4M3(x) and x2 = E4M3(x - x1), which holds a bf16 value without loss (its
+// rows scaled by a power of two, down to 2^-10 of the row's largest value).  P, whose small
+// weights count where there are many: x1 = E5M2(x) and x2 = E4M3(x - x1), with 2^9 at the row's
+// reference.  That is bf16's half a step, 2^-8 of a weight, down to 2^-11 of the row's largest,
+// and 2^-3 of it, to nearest, down to 2^-23 (0 below 2^-26).  With both parts in E4M3 and 64 at
+// the reference a weight was within 2^-9, but 0 below 2^-16: of 8191 tokens 12 nats below a
+// first one a quarter of the result was missing.  Codes take half the bytes of bf16 rows on the way and in shared memory, so three
 // buffers fit instead of two.  Widening them to f16 in front of the MMAs instead, by eight warps
 // of each CTA, took 6,700 cycles a tile: they waited for their own loads.
 //
@@ -90,11 +93,13 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemO = 0;    // O': column 128 h + c of lane l is latent column 256 (l / 64) + 128 h + c
 constexpr uint32_t kTmemS = 256;  // two score buffers of 64 columns
 constexpr uint32_t kTmemR = 384;  // FP8: the RoPE part of the scores, two buffers as well
-// O' is rescaled where a row's maximum grows by more than this.  The FP8 form's P is kPUp at the
-// reference and must stay below E4M3's 448.
-constexpr float kPUp = 64.f;
+// O' is rescaled where a row's maximum grows by more than this.  The FP8 form's P is 2^kPUpLog2 at the
+// reference and must stay below 2^12, from where on what E5M2 leaves over passes E4M3's 448.
+template <bool kFp8>
+constexpr float kPUpLog2 = kFp8 ? 9.f : 0.f;
 template <bool kFp8>
 constexpr float kRescaleLog2 = kFp8 ? 2.8f : 8.f;
+static_assert(kPUpLog2<true> + kRescaleLog2<true> < 12.f, "P in two parts");
 constexpr int kOutPitch = 4 * kLatent + 16;  // a row of O' on its way out
 static_assert(kOffX + kRows * kOutPitch <= kOffP, "rows of O' in the tiles' place");
 constexpr uint16_t kBoth = 0x3;
@@ -191,6 +196,13 @@ __device__ __forceinline__ void split_e4m3(uint32_t x, uint16_t& x1, uint16_t& x
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(x1) : "r"(x));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(x1));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(x), "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(x2) : "r"(rest));
+}
+// The same of a weight's pair (not negative): E5M2 is an f16's upper byte, rounded.
+__device__ __forceinline__ void split_e5m2(uint32_t x, uint16_t& x1, uint16_t& x2) {
+  uint32_t rest;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(x1) : "r"(x));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(x), "r"(__byte_perm(x1, 0, 0x1404)));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(x2) : "r"(rest));
 }
 // A bf16 pair times k as f16.
@@ -415,6 +427,7 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // 16-bit operands of the RoPE product (FP8: f16) and, of a bf16 cache, of all the others
       const uint32_t idesc_s = kFp8 ? idesc_f16(128, 128, /*a_mn=*/0, /*b_mn=*/0) : idesc_bf16(128, 128, 0, 0);
       const uint32_t idesc_o = kFp8 ? idesc_f16(128, 256, /*a_mn=*/0, /*b_mn=*/1) : idesc_bf16(128, 256, 0, 1);
+      constexpr uint32_t kE5m2A = 1u << 7;  // (FP8) P's first part
       const uint64_t d_q = smem_desc(smem_u32(smem + kOffQ), 16, 1024, kSw128);
       const uint64_t d_k = smem_desc(smem_u32(smem + kOffX), 16, 1024, kSw128);      // keys (K-major)
       const uint64_t d_r = smem_desc(smem_u32(smem + kOffR), 16, 1024, kSw128);
@@ -481,7 +494,7 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (kFp8) {  // two steps of 32 tokens, P's two parts
                   const int step = k >> 1, part = k & 1;
                   mma2_ss_f8(tmem + kTmemO + 128 * h, d_p + part * kC + 2 * (2 * pg + step), vb + h * kC + 256 * step,
-                             idesc_o, acc);
+                             idesc_o | (part == 0 ? kE5m2A : 0u), acc);
                 } else {  // four steps of 16 tokens
                   mma2_ss(tmem + kTmemO + 128 * h, d_p + pg * kC + 2 * k, vb + h * 2 * kC + 128 * k, idesc_o, acc);
                 }
@@ -678,7 +691,7 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         m = mx;
         rescale = true;
       }
-      const float neg_m = m == -INFINITY ? 0.f : -m;
+      const float neg_m = kPUpLog2<kFp8> - (m == -INFINITY ? 0.f : m);
       const uint64_t neg2 = f32x2(neg_m, neg_m);
       uint32_t pk[16];
       uint64_t s2[2] = {0ull, 0ull};
@@ -690,8 +703,8 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         s2[c & 1] = add_f32x2(s2[c & 1], f32x2(p0, p1));
         if (kFp8) {  // words c / 2 of both parts; P carries s_t, the row sum does not
           uint16_t x1, x2;
-          const float2 y = f32x2_split(mul_f32x2(f32x2(p0 * kPUp, p1 * kPUp), f32x2(st[c].x, st[c].y)));
-          split_e4m3(pack_f16x2(y.x, y.y), x1, x2);
+          const float2 y = f32x2_split(mul_f32x2(f32x2(p0, p1), f32x2(st[c].x, st[c].y)));
+          split_e5m2(pack_f16x2(y.x, y.y), x1, x2);
           if (c & 1) {
             pk[c >> 1] = half1 | static_cast<uint32_t>(x1) << 16;
             pk[8 + (c >> 1)] = half2 | static_cast<uint32_t>(x2) << 16;
@@ -762,9 +775,9 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       l = (hb[0] + hb[kRows]) + (hb[2 * kRows] + hb[3 * kRows]);
     }
     const bool some = ok && tiles > 0 && l != 0.f;
-    const float inv = some ? 1.f / (kFp8 ? l * kPUp : l) : 0.f;
+    const float inv = some ? 1.f / l : 0.f;
     if (slot == 0 && p.lse_out != nullptr) {
-      float lse = some ? (m + log2f(l)) * kLn2 : -INFINITY;
+      float lse = some ? (m - kPUpLog2<kFp8> + log2f(l)) * kLn2 : -INFINITY;
       // a visible NaN: the merge leaves out a split whose weight is NaN, but not one that makes all of them 0 / 0
       if (p.num_splits > 1 && lse != lse) lse = INFINITY;
       p.lse_out[out_row] = lse;

@@ -1,9 +1,11 @@
 """Attention over the FP8 cache where a row's weights, its tokens' scales or its query's two parts span many powers of two,
 against the plain float64 definition on the values that the cache stands for.
 
-Tolerances.  A weight times its token's scale is rounded to 8 bits (half a step, 2^-8 of it, uniform at the worst:
-2^-8 / sqrt(3) = 2.3e-3 rms), and the output likewise: 3.2e-3, and the repository's 5e-3 for a head by itself, relative
-L2 of its O' and of its outputs."""
+Tolerances.  A weight times its token's scale is rounded to 8 bits down to 2^-11 of the row's largest one (half a step,
+2^-8 of it, uniform at the worst: 2^-8 / sqrt(3) = 2.3e-3 rms), and the output likewise: 3.2e-3, and the repository's
+5e-3 for a head by itself, relative L2 of its O' and of its outputs.  Smaller weights have 3 bits down to 2^-26 (2^-3 /
+sqrt(3) = 0.072 rms of each, signs at random).  Where n tokens share the weight, their sum is off by 0.072 / sqrt(n): 8e-4
+for 8191 of them, 4.8e-3 at six deviations: 5e-3 again."""
 
 import numpy as np
 import pytest
@@ -60,4 +62,22 @@ def test_large_scales_with_low_scores(shift):
         c[far, 511], k[far, 0] = 448.0 * 2.0 ** (shift - 7), -64.0
         fill(p, b, c, k, s)
     p.q[..., 511], p.q[..., 512] = 0.0, 8.0  # 8 x -64 / sqrt(192) = -37
+    check(p)
+
+
+@pytest.mark.parametrize("first", [1.0, 0.1])
+def test_many_weak_tokens_behind_a_strong_one(first):
+    """A first token that outweighs each other one by 8 to 17 nats (a head each), over values that share a mean: the weak
+    ones' sum counts, and what a kernel loses of it does not cancel."""
+    p = Problem([8191], 1, seed=1, fp8=True)
+    g = torch.Generator().manual_seed(2)
+    c, k = 1.0 + 0.3 * torch.randn(8192, 512, generator=g), torch.zeros(8192, 64)
+    k[:, 0] = -(1.0 + 0.05 * torch.randn(8192, generator=g))
+    c[0], k[0] = first, 0.0
+    fill(p, 0, c, k)
+    lat = torch.randn(128, 512, generator=g) * 0.226
+    p.q[0, 0, :, :512] = (lat - lat.mean(1, keepdim=True)).to(torch.bfloat16)
+    p.q[0, 0, :, 512:] = 0.0
+    p.q[0, 0, :, 512] = (torch.linspace(8.0, 17.0, 128) * 192 ** 0.5).to(torch.bfloat16)
+    # |q| |row| <= 236 x 1.2 + 6 x 24: 430, against 576 in the plain inputs
     check(p)
