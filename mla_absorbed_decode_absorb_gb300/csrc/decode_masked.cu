@@ -533,12 +533,15 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     float* logs = reinterpret_cast<float*>(smem + kOffLog2) + 32 * warp;  // (the warp's 32 tokens are the same in all its rows)
     const uint32_t s_free = mapa(smem_u32(&bars.s_free[0]), 0), p_full = mapa(smem_u32(&bars.p_full[0]), 0);
     float score_log2 = kScaleLog2;  // a score's factor, in exponents of 2
+    float rot_factor = 1.f;         // FP8: and that of its RoPE part, to the latent part's units
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (kFp8 && tiles > 0) {
-      // The query in place: the latent columns times 2^a as two E4M3 parts, the RoPE columns times 2^a as
-      // f16, with the row's a bringing its largest latent value into [128, 256) (and the RoPE columns
-      // below 2^15).  This thread takes bf16 chunks 2 quarter and 2 quarter + 1 and 16 RoPE columns.
+      // The query in place: the latent columns times 2^a as two E4M3 parts, the RoPE columns times 2^ar as
+      // f16, with the row's a bringing its largest latent value into [128, 256) and its ar the largest RoPE
+      // value into [2^14, 2^15).  Their scores meet in the softmax.  (Latent values 2^60 below the RoPE ones are
+      // given up, so that the factor between the two stays in range.)  This thread takes bf16 chunks 2 quarter
+      // and 2 quarter + 1 and 16 RoPE columns.
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.q_land), 0, p.status, abort));
       uint8_t* q = smem + kOffQ + r * 128;
       auto unit = [&](int chunk, int u) { return reinterpret_cast<uint4*>(q + chunk * kChunk + ((u ^ (r & 7)) << 4)); };
@@ -569,9 +572,11 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         top_rot = max(top_rot, t & 0xffffu);
       }
       const int e_lat = static_cast<int>(top_lat >> 7) - 127, e_rot = static_cast<int>(top_rot >> 7) - 127;
-      const int a = max(-100, min(100, min(7 - e_lat, 14 - e_rot)));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
-      score_log2 *= __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+      const int ar = min(100, 14 - e_rot), a = min(min(100, 7 - e_lat), ar + 60);
+      auto power = [](int e) { return __uint_as_float(static_cast<uint32_t>(127 + max(-126, e)) << 23); };
+      const float up = power(a), up_rot = power(ar);
+      score_log2 *= power(-a);
+      rot_factor = power(a - ar);
       if (e_lat == 128 || e_rot == 128) score_log2 = NAN;  // an infinity or a NaN (E4M3 would saturate)
 #pragma unroll
       for (int u = 0; u < 8; ++u) {  // 16 columns: two units of bf16 in, one of each part out
@@ -591,14 +596,14 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        *unit(8, 2 * quarter + u) = make_uint4(bf16x2_to_f16x2(rot[u].x, up), bf16x2_to_f16x2(rot[u].y, up),
-                                               bf16x2_to_f16x2(rot[u].z, up), bf16x2_to_f16x2(rot[u].w, up));
+        *unit(8, 2 * quarter + u) = make_uint4(bf16x2_to_f16x2(rot[u].x, up_rot), bf16x2_to_f16x2(rot[u].y, up_rot),
+                                               bf16x2_to_f16x2(rot[u].z, up_rot), bf16x2_to_f16x2(rot[u].w, up_rot));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_pair(mapa(smem_u32(&bars.q_full), 0));
       named_barrier_sync(1, kSoftThreads);  // hx has been read
     }
-    const uint64_t scale2 = f32x2(score_log2, score_log2);
+    const uint64_t scale2 = f32x2(score_log2, score_log2), rot2 = f32x2(rot_factor, rot_factor);
     for (int i = 0; i < tiles; ++i) {
       const int buf = i & 1;
       const bool there = 2 * i + hf < n;  // the tile has this thread's page
@@ -635,7 +640,12 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tmem_ld32(tmem + lane_off + kTmemR + 64 * buf + 32 * ch, rot);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) sv[c] = __uint_as_float(a[c]) + __uint_as_float(rot[c]);
+          for (int c = 0; c < 32; c += 2) {
+            const float2 f = f32x2_split(fma_f32x2(f32x2(__uint_as_float(rot[c]), __uint_as_float(rot[c + 1])), rot2,
+                                                   f32x2(__uint_as_float(a[c]), __uint_as_float(a[c + 1]))));
+            sv[c] = f.x;
+            sv[c + 1] = f.y;
+          }
         } else {
           tmem_wait_ld();
 #pragma unroll

@@ -81,3 +81,18 @@ def test_many_weak_tokens_behind_a_strong_one(first):
     p.q[0, 0, :, 512] = (torch.linspace(8.0, 17.0, 128) * 192 ** 0.5).to(torch.bfloat16)
     # |q| |row| <= 236 x 1.2 + 6 x 24: 430, against 576 in the plain inputs
     check(p)
+
+
+@pytest.mark.parametrize("x", [0, 4, 8, 12])
+def test_a_query_whose_parts_differ_in_size(x):
+    """Latent columns 2^x times smaller and rotated ones 2^x times larger, over rows the other way round: scores as ever,
+    of which each part has half."""
+    p = Problem([300, 64], 2, seed=x, fp8=True)
+    g = torch.Generator().manual_seed(x)
+    for b in range(p.B):
+        n = p.prior[b] + p.n_q
+        fill(p, b, torch.randn(n, 512, generator=g) * 2.0 ** x, torch.randn(n, 64, generator=g) * 2.0 ** -x)
+    p.q[..., :512] *= 2.0 ** -x
+    p.q[..., 512:] *= 2.0 ** x
+    p.w_uv = (p.w_uv.float() * 2.0 ** -x).to(torch.bfloat16)
+    check(p)
