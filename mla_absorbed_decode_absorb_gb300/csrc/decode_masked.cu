@@ -264,7 +264,7 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     uint32_t* keys = reinterpret_cast<uint32_t*>(smem + kOffP);  // length, then place
     if (tid < kMostSorted) {
       const int pages = tid < p.longest_first
-                            ? min((max(p.kv_lens[tid / p.num_splits], 0) + kPage - 1) / kPage, p.max_pages) -
+                            ? min(pages_of(max(p.kv_lens[tid / p.num_splits], 0)), p.max_pages) -
                                   (tid % p.num_splits) * p.split_pages
                             : 0;
       const int length = min(max(pages, 0), min(p.split_pages, 1 << 20));
@@ -291,8 +291,7 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint64_t word = p.words != nullptr ? p.words[bj] & low_bits(p.n_q) : low_bits(j + 1);
   const int depth = p.depths != nullptr ? p.depths[bj] : j;
   const bool used = word != 0;  // a node that sees nothing is not part of the tree
-  const bool bad = used && (kv > p.max_kv_len || kv < p.n_q || (kv + kPage - 1) / kPage > p.pt_stride || depth < 0 ||
-                            depth >= p.n_q);
+  const bool bad = used && (kv > p.max_kv_len || kv < p.n_q || pages_of(kv) > p.pt_stride || depth < 0 || depth >= p.n_q);
   QueryView v{};
   if (used && !bad) v = make_view(kv - p.n_q, kv - p.n_q + depth, word, p.words == nullptr, p.window, p.sinks);
   const int k0 = split * p.split_pages;

@@ -15,6 +15,8 @@ constexpr int kLatent = MLA_D_LATENT;  // d_c
 constexpr int kRope = MLA_D_ROPE;      // d_h^R
 constexpr int kRow = MLA_D_ROW;        // d_c + d_h^R
 constexpr int kPage = MLA_PAGE;
+// Pages that hold `tokens` (>= 0) tokens; tokens + kPage - 1 would pass 32 bits for the last 63 lengths.
+__host__ __device__ constexpr int pages_of(int tokens) { return tokens / kPage + (tokens % kPage != 0); }
 constexpr int kHalfRope = kRope / 2;
 // 1/sqrt(d_h + d_h^R) and that times log2(e): scores are exponentiated with exp2.
 constexpr float kScale = 0.07216878364870323f;         // 1/sqrt(192)

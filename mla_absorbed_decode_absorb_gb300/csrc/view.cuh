@@ -36,7 +36,7 @@ __device__ __forceinline__ QueryView make_view(int L, int pos, uint64_t word, bo
     return v;
   }
   v.w0 = min(v.lo, end - 1) / kPage;
-  v.ns = min((v.sink_hi + kPage - 1) / kPage, v.w0);  // the sinks' last page may be the window's first
+  v.ns = min(pages_of(v.sink_hi), v.w0);  // the sinks' last page may be the window's first
   v.n_pages = v.ns + (end - 1) / kPage - v.w0 + 1;
   return v;
 }
@@ -56,7 +56,7 @@ __device__ __forceinline__ uint64_t view_bits(const QueryView& v, int page) {
 // The most pages a view holds, over every query of a sequence of at most max_kv_len
 // tokens: all of them, or the sinks' and a window's that starts anywhere in a page.
 inline int max_view_pages(int n_q, int max_kv_len, int window, int sinks) {
-  const int all = (max_kv_len + kPage - 1) / kPage;
+  const int all = pages_of(max_kv_len);
   if (window <= 0) return all;
   const int64_t span = static_cast<int64_t>(window) + n_q - 1;  // oldest token of the first query .. the last new one
   const int64_t pages = (sinks + static_cast<int64_t>(kPage) - 1) / kPage + (span + kPage - 2) / kPage + 1;
