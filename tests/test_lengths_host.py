@@ -36,3 +36,26 @@ def test_masked_plans_of_the_longest_lengths(lib, length):
             view = min(pages, (window + 2 + 62) // 64 + 1 + -(-sinks // 64))
             n = asked(lib.mla_masked_num_splits, I(0), 2, 3, length, window, sinks, split)
             assert 1 <= n <= 64 and (split < 8 or window == LONGEST or n == -(-view // split))
+
+
+A = 1 << 20  # a valid-looking address: every check comes before the device is touched
+
+
+@pytest.mark.parametrize("B,n_q,max_kv_len,window,sinks,split", [
+    (4, 3, 1000, 0, 0, 4), (1, 1, 4096, 0, 0, 1), (3, 64, 5000, 700, 5, 3), (129, 7, 300, 0, 0, 2)])
+def test_masked_workspace_holds_the_partials_and_no_less(lib, B, n_q, max_kv_len, window, sinks, split):
+    """512 float32 values and a float32 log-sum-exp of each query, split and head, either rounded up to 256 bytes; one byte
+    less is refused."""
+    plan = (B, n_q, max_kv_len, window, sinks, split)
+    n = asked(lib.mla_masked_num_splits, I(0), *plan)
+    size = asked(lib.mla_masked_workspace_size, SZ(0), *plan)
+    rows = B * n_q * n * 128
+    assert n > 1 and rows * (512 * 4 + 4) <= size < rows * (512 * 4 + 4) + 2 * 256
+    attend = lib.mla_decode_attn_masked_partial
+    attend.argtypes = [P, P, I64, P, I, P, P, P, I, I, I, I, I, I, P, SZ, P, P, P]
+    pages = -(-max_kv_len // 64)
+
+    def args(ws, b):
+        return A, A, pages, A, pages, A, None, None, window, sinks, B, n_q, max_kv_len, split, ws, b, A, A, None
+    assert attend(*args(A, size - 1)) == WORKSPACE and attend(*args(None, size)) == WORKSPACE
+    assert attend(*args(A + 8, size)) == WORKSPACE
