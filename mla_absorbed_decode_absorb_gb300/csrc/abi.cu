@@ -160,7 +160,7 @@ bool device_view(const void* p, size_t bytes, void** out, bool* host) {
 // a unit's fixed cost (query load, pipeline fill, epilogue, partial write).
 bool make_plan(int B, int n_q, int max_kv_len, int split_pages, SplitPlan* plan) {
   if (B < 0 || n_q < 1 || n_q > MLA_MAX_NQ || max_kv_len < n_q || split_pages < 0) return false;
-  plan->max_pages = (max_kv_len + kPage - 1) / kPage;
+  plan->max_pages = pages_of(max_kv_len);
   plan->short_path = split_pages == 0 && max_kv_len <= kShortMaxKv &&
                      static_cast<int64_t>(B) * n_q <= kShortMaxUnits;
   if (plan->short_path) split_pages = plan->max_pages;  // one split: no merge
@@ -180,8 +180,8 @@ bool make_plan(int B, int n_q, int max_kv_len, int split_pages, SplitPlan* plan)
       }
     }
   }
-  plan->split_pages = split_pages;
-  plan->num_splits = (plan->max_pages + split_pages - 1) / split_pages;
+  plan->split_pages = split_pages < plan->max_pages ? split_pages : plan->max_pages;
+  plan->num_splits = (plan->max_pages + plan->split_pages - 1) / plan->split_pages;
   const size_t rows = static_cast<size_t>(B) * n_q * plan->num_splits * kHeads;
   plan->o_part_bytes = round_up(rows * kLatent * sizeof(uint16_t), 256);  // bf16 partials
   plan->lse_part_bytes = round_up(rows * sizeof(float), 256);

@@ -258,11 +258,12 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_
 
   // The unit's token range [t_begin, t_end): identical in both CTAs of the cluster.
   const int kv = p.kv_lens[b];
-  const bool bad = kv > p.max_kv_len || kv < p.n_q || (kv + kPage - 1) / kPage > p.pt_stride;
+  const bool bad = kv > p.max_kv_len || kv < p.n_q || pages_of(kv) > p.pt_stride;
   const int t_begin = split * p.split_pages * kPage;
-  const int t_end = bad ? t_begin : min(t_begin + p.split_pages * kPage, kv - p.n_q + j + 1);
+  const int seen = bad ? 0 : kv - p.n_q + j + 1;  // (compared in pages: a split's end may pass 32 bits)
+  const int t_end = pages_of(seen) - split * p.split_pages > p.split_pages ? t_begin + p.split_pages * kPage : seen;
   const int page_begin = t_begin / kPage;
-  const int n_pages = t_end > t_begin ? (t_end + kPage - 1) / kPage - page_begin : 0;
+  const int n_pages = t_end > t_begin ? pages_of(t_end) - page_begin : 0;
   if (tid == 0 && bad && rank == 0) record_status(p.status, MLA_ERR_BOUNDS);
   // the peer's barriers exist before any remote traffic (the first partial
   // scores, long after the loads above are on their way)

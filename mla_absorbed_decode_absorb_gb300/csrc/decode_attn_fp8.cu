@@ -191,11 +191,12 @@ decode_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_q64, const __grid_
   grid_dep_launch();
 
   const int kv = p.kv_lens[b];
-  const bool bad = kv > p.max_kv_len || kv < p.n_q || (kv + kPage - 1) / kPage > p.pt_stride;
+  const bool bad = kv > p.max_kv_len || kv < p.n_q || pages_of(kv) > p.pt_stride;
   const int t_begin = split * p.split_pages * kPage;
-  const int t_end = bad ? t_begin : min(t_begin + p.split_pages * kPage, kv - p.n_q + j + 1);
+  const int seen = bad ? 0 : kv - p.n_q + j + 1;  // (compared in pages: a split's end may pass 32 bits)
+  const int t_end = pages_of(seen) - split * p.split_pages > p.split_pages ? t_begin + p.split_pages * kPage : seen;
   const int page_begin = t_begin / kPage;
-  const int n_pages = t_end > t_begin ? (t_end + kPage - 1) / kPage - page_begin : 0;
+  const int n_pages = t_end > t_begin ? pages_of(t_end) - page_begin : 0;
   if (tid == 0 && bad && rank == 0) record_status(p.status, MLA_ERR_BOUNDS);
 
   if (warp == kProducerWarp) {

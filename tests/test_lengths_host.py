@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-OK, INVALID, WORKSPACE = 0, 1, 3
+OK, WORKSPACE = 0, 3
 I, SZ, P, I64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int64
 LONGEST = 2 ** 31 - 1
 
@@ -59,3 +59,14 @@ def test_masked_workspace_holds_the_partials_and_no_less(lib, B, n_q, max_kv_len
         return A, A, pages, A, pages, A, None, None, window, sinks, B, n_q, max_kv_len, split, ws, b, A, A, None
     assert attend(*args(A, size - 1)) == WORKSPACE and attend(*args(None, size)) == WORKSPACE
     assert attend(*args(A + 8, size)) == WORKSPACE
+
+
+@pytest.mark.parametrize("length", [LONGEST, LONGEST - 1, LONGEST - 62, LONGEST - 63, LONGEST - 64])
+def test_causal_plans_of_the_longest_lengths(lib, length):
+    pages = -(-length // 64)
+    for split in (0, 1, 1000, 1 << 20, 1 << 25, LONGEST - 1, LONGEST):
+        n = asked(lib.mla_decode_num_splits, I(0), 2, 3, length, split)
+        assert n == -(-pages // split) if split else 1 <= n <= 256
+        size = asked(lib.mla_decode_workspace_size, SZ(0), 2, 3, length, split)
+        assert size >= (2 * 3 * n * 128 * (512 * 2 + 4) if n > 1 else 0)
+    assert asked(lib.mla_decode_num_splits, I(0), 8, 4, 300, LONGEST) == 1  # one split of all pages
