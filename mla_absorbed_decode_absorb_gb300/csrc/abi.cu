@@ -666,7 +666,7 @@ mla_status mla_decompress_kv(const mla_bf16* cache, int64_t num_pages, const int
                              const int32_t* kv_lens, int B, int max_kv_len, const mla_bf16* w_uk,
                              const mla_bf16* w_uv, mla_bf16* k_nope, mla_bf16* v, cudaStream_t stream) {
   if (B < 0 || max_kv_len < 0 || num_pages < 0 || pt_stride < 0) return MLA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(B) * kHeads * (max_kv_len + kPage) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * kHeads * (static_cast<int64_t>(max_kv_len) + kPage) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if (B == 0 || max_kv_len == 0) return MLA_OK;
   if (!cache || !page_table || !kv_lens || !w_uk || !w_uv || !k_nope || !v) return MLA_ERR_INVALID_ARG;
   if (!aligned16(cache) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(k_nope) || !aligned16(v))
@@ -685,7 +685,7 @@ mla_status mla_prefill_attn(const mla_bf16* q_nope, const mla_bf16* q_rope, cons
                             cudaStream_t stream) {
   if (B < 0 || n_q < 0 || max_kv_len < n_q || num_pages < 0 || pt_stride < 0 || rope_max_pos < 0)
     return MLA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(B) * kHeads * (max_kv_len + 128) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * kHeads * (static_cast<int64_t>(max_kv_len) + 128) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if (B == 0 || n_q == 0) return MLA_OK;
   if (!q_nope || !q_rope || !seq_lens_before || !rope_table || !k_nope || !v || !cache || !page_table ||
       !kv_lens || !out)

@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-OK, WORKSPACE = 0, 3
+OK, UNSUPPORTED, WORKSPACE = 0, 2, 3
 I, SZ, P, I64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int64
 LONGEST = 2 ** 31 - 1
 
@@ -70,3 +70,19 @@ def test_causal_plans_of_the_longest_lengths(lib, length):
         size = asked(lib.mla_decode_workspace_size, SZ(0), 2, 3, length, split)
         assert size >= (2 * 3 * n * 128 * (512 * 2 + 4) if n > 1 else 0)
     assert asked(lib.mla_decode_num_splits, I(0), 8, 4, 300, LONGEST) == 1  # one split of all pages
+
+
+@pytest.mark.parametrize("length", [LONGEST, LONGEST - 64, LONGEST - 127, LONGEST - 128, 1 << 24])
+def test_prompts_of_the_longest_lengths_are_refused(lib, length):
+    """128 heads' rows of one sequence pass 32 bits."""
+    stride = 1 << 25
+    decompress, attend = lib.mla_decompress_kv, lib.mla_prefill_attn
+    decompress.argtypes = [P, I64, P, I, P, I, I, P, P, P, P, P]
+    attend.argtypes = [P, P, P, P, I, P, P, I, P, I64, P, I, P, I, I, P, P, P]
+    assert decompress(A, 8, A, stride, A, 1, length, A, A, A, A, None) == UNSUPPORTED
+    assert attend(A, A, A, A, 300, A, A, length, A, 8, A, stride, A, 1, 70, A, A, None) == UNSUPPORTED
+    windowed, prompt = lib.mla_decompress_kv_window, lib.mla_prefill_attn_window
+    windowed.argtypes = [P, I64, P, I, P, I, I, I, I, I, P, P, P, P, P]
+    prompt.argtypes = [P, P, P, P, I, P, P, I, P, I64, P, I, P, I, I, I, I, P, P, P]
+    assert windowed(A, 8, A, stride, A, 1, 70, length, 64, 4, A, A, A, A, None) == UNSUPPORTED
+    assert prompt(A, A, A, A, 300, A, A, length, A, 8, A, stride, A, 1, 70, 64, 4, A, A, None) == UNSUPPORTED
