@@ -137,8 +137,9 @@ __device__ __forceinline__ bool next_tile(const Params& p, const int* meta, int&
     t.qt = second ? pr : q_hi;
     t.L = meta != nullptr ? meta[t.b] : p.seq_lens_before[t.b];
     t.kv = meta != nullptr ? meta[kMetaCap + t.b] : p.kv_lens[t.b];
-    t.bad = t.L < 0 || t.kv != t.L + p.n_q || t.kv > p.max_kv_len || (t.kv + kPage - 1) / kPage > p.pt_stride ||
-            t.L + p.n_q > p.rope_max_pos;
+    // (kv - n_q, which cannot wrap behind the first check: L + n_q may, onto a kv that did)
+    t.bad = t.kv < p.n_q || t.kv - p.n_q != t.L || t.kv > p.max_kv_len || pages_of(t.kv) > p.pt_stride ||
+            t.kv > p.rope_max_pos;
     t.j0 = t.qt * kQTile;
     const int j_last = min(p.n_q, t.j0 + kQTile) - 1;  // last query of the tile
     t.n_kt = t.bad ? 0 : (t.L + j_last + 1 + kKTile - 1) / kKTile;

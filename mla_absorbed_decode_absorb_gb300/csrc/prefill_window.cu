@@ -208,9 +208,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         const int j1 = min(p.n_q, u.j0 + (cut ? 1 : 2) * kTile);  // behind its last query
         u.L = p.seq_lens_before[u.b];
         u.kv = p.kv_lens[u.b];
-        if (u.L < 0 || u.kv != u.L + p.n_q || u.kv > p.max_kv_len || (u.kv + kPage - 1) / kPage > p.pt_stride ||
+        if (u.kv < p.n_q || u.kv - p.n_q != u.L || u.kv > p.max_kv_len || pages_of(u.kv) > p.pt_stride ||
             u.kv > p.rope_max_pos) {
-          // an invalid sequence: O = 0 and lse = -inf
+          // an invalid sequence: O = 0 and lse = -inf.  (L + n_q may wrap, onto a kv that did; kv - n_q may not here.)
           if (lane == 0) record_status(p.status, MLA_ERR_BOUNDS);
 #pragma unroll 1
           for (int j = u.j0; j < j1; ++j) {

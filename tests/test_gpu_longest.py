@@ -64,3 +64,20 @@ def test_causal_attention(fp8, split):
         out, lse = run(LONGEST, split, torch.tensor([3, long, 5003], dtype=torch.int32, device="cuda"))
         assert status() == MLA_ERR_BOUNDS
         assert not out[1].any() and torch.isneginf(lse[1]).all()
+
+
+@pytest.mark.parametrize("past", [1, 70])
+def test_prompts_behind_a_context_that_wraps(past):
+    """seq_lens_before so large that n_q more pass 32 bits, and kv_lens the sum that has: reported, and zeros."""
+    from mla_absorbed_decode_absorb_gb300 import ops
+    from test_gpu_view import prompt
+    n_q = 70
+    out, lse, (q, r, lens, rope, cache, table, kv, uk, uv, max_kv) = prompt([100, 100], n_q, 50, 4, 6, poison=False)
+    k, v = ops.mla_decompress_kv(cache, table, kv, max_kv, uk, uv)
+    lens, kv = lens.clone(), kv.clone()
+    lens[1], kv[1] = 2 ** 31 - past, n_q - past - 2 ** 31
+    for call, args in ((ops.mla_prefill_attn, ()), (ops.mla_prefill_attn_window, (50, 4))):
+        got_lse = torch.empty_like(lse)
+        got = call(q, r, lens, rope, k, v, cache, table, kv, *args, None, got_lse)
+        assert status() == MLA_ERR_BOUNDS
+        assert not got[1].any() and torch.isneginf(got_lse[1]).all() and torch.isfinite(got_lse[0]).all()
