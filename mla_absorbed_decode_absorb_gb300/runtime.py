@@ -130,8 +130,7 @@ class DecodeSession:
                 raise ValueError(f"a tree takes the absorbed path, up to {ops.MLA_MAX_TREE} nodes a sequence")
             if overlap_append or not fused_prologue:
                 raise ValueError("a tree's rows are appended beside its absorbed query")
-            if tuple(tree.shape) != (self.B, self.n_q):
-                raise ValueError(f"tree must have shape {(self.B, self.n_q)}, got {tuple(tree.shape)}")
+            self._check_tree(tree)
         if self.masked and path == "absorbed" and not fused_finish:
             raise ValueError("a tree's or a window's splits are merged in the out-projection's launch")
         self._parents = tree
@@ -237,9 +236,16 @@ class DecodeSession:
     def _main(self, stream):
         return ops._torch_stream(stream, self.device)
 
+    def _check_tree(self, parents):
+        if not self.tree:
+            raise ValueError("only a session laid out with a tree takes another one")
+        if tuple(parents.shape) != (self.B, self.n_q):
+            raise ValueError(f"a tree's parents must have shape {(self.B, self.n_q)}, got {tuple(parents.shape)}")
+
     def set_tree(self, parents: torch.Tensor, stream=None):
         """The next steps' trees: parents [B, n_q], into this session's buffers (a captured step uses them too).  With a
         window, what a node sees goes by ``prior_lens`` as they are when this runs: set those first."""
+        self._check_tree(parents)
         with ops._on(stream):
             self.parents.copy_(parents, non_blocking=parents.is_cuda)
         ops.mla_tree_prepare(self.parents, self.prior_lens, self.window, self.sinks, self.depths, self.tree_mask,
