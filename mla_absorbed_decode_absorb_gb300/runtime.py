@@ -131,6 +131,9 @@ class DecodeSession:
             if overlap_append or not fused_prologue:
                 raise ValueError("a tree's rows are appended beside its absorbed query")
             self._check_tree(tree)
+        if self.masked and not self.tree and path == "absorbed" and self.n_q > ops.MLA_MAX_NQ:
+            raise ValueError(f"a window without a tree takes the absorbed path with up to {ops.MLA_MAX_NQ} new tokens a "
+                             "sequence (a tree that is a chain: up to the tree's limit)")
         if self.masked and path == "absorbed" and not fused_finish:
             raise ValueError("a tree's or a window's splits are merged in the out-projection's launch")
         self._parents = tree

@@ -37,3 +37,17 @@ def test_a_session_without_a_tree_takes_none(rec, kw):  # noqa: F811
         s = session([5], 3, **kw)
     with pytest.raises(ValueError):
         s.set_tree(chain(1, 3))
+
+
+def test_more_new_tokens_than_the_causal_append_takes_are_refused_at_once(rec):  # noqa: F811
+    """The absorbed path of a window appends at most eight tokens a sequence; a chain given as a tree goes further, and so
+    does the other path."""
+    with pytest.raises(ValueError), rec:
+        session([5, 70], 9, window=20, path="absorbed")
+    with rec:
+        assert session([5, 70], 8, window=20, path="absorbed").path == "absorbed"
+        assert session([5, 70], 9, window=20).path == "non_absorbed"
+        s = session([5, 70], 9, window=20, tree=chain(2, 9))
+        rec.log.clear()
+        s.step()
+    assert s.path == "absorbed" and [n for kind, n, _ in rec.log if kind == "launch"][0] == "mla_append_absorb_q_tree"
