@@ -28,11 +28,13 @@ constexpr int kManyTokens = 33;  // 64 tokens: 10.2 us against 12.5 for the othe
 constexpr int kFixedTiles = 6, kTileNs = 1450;
 // What the merge of splits adds to the finish: by its bytes in the kernel for many tokens; in the other one a split's
 // turn, and 7 us for every further wave of its CTAs, which hold 64 rows each (8 tokens of 8 splits 8.4 us, of 9 16.9).
-inline int64_t merge_ns(int64_t queries, int splits) {
+// Waves are counted over the SMs that pairs of CTAs fill, 148 of the 152 here; over all of them a few plans of very long
+// contexts had one split more and took 1 to 2% longer (16 x 5 tokens of 32000: 544 us for 534).
+inline int64_t merge_ns(int64_t queries, int splits, int64_t slots) {
   if (splits == 1) return 0;
   if (splits <= 2 && queries >= kManyTokens) return 30 * queries * splits;
   const int64_t tile = splits > 2 ? 64 / splits : 32, ctas = kHeads * ((queries + tile - 1) / tile);
-  return 100 * splits + 7000 * ((ctas - 1) / 148);
+  return 100 * splits + 7000 * ((ctas - 1) / (2 * slots));
 }
 
 mla_status masked_plan(int B, int n_q, int max_kv_len, int window, int sinks, int split_pages, SplitPlan* plan) {
@@ -49,7 +51,7 @@ mla_status masked_plan(int B, int n_q, int max_kv_len, int window, int sinks, in
     for (int s = 1; s <= max_tiles && s <= 64; ++s) {
       const int tiles = (max_tiles + s - 1) / s;
       const int64_t waves = (units * ((max_tiles + tiles - 1) / tiles) + slots - 1) / slots;
-      int64_t cost = waves * (tiles + kFixedTiles) * kTileNs + merge_ns(units, (max_tiles + tiles - 1) / tiles);
+      int64_t cost = waves * (tiles + kFixedTiles) * kTileNs + merge_ns(units, (max_tiles + tiles - 1) / tiles, slots);
       if (tiles < max_tiles && units > slots) cost += cost / 6;
       if (best < 0 || cost < best) {
         best = cost;
