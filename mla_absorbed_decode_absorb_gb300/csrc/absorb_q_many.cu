@@ -259,6 +259,7 @@ absorb_q_many_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     }
     if (leader) bulk_wait_all();
   }
+  if (*abort) let_work_land();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);

@@ -817,6 +817,7 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       bulk_wait_read<0>();  // (the writes themselves are complete at the kernel's end)
     }
   }
+  if (*abort) let_work_land();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the pair's MMAs have finished, and nobody addresses the other CTA any more

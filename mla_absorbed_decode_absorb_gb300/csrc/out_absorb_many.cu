@@ -243,6 +243,7 @@ out_absorb_many_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
       if (kSplits == 2) ok = named_barrier_and(1, kMergeThreads, ok);
     }
   }
+  if (*abort) let_work_land();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 256);

@@ -93,6 +93,13 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   return mbar_wait_impl<true>(bar, parity, status, abort);
 }
 
+// Behind a wait that ran out: a millisecond for the copies and products still under way, before the CTA's shared and
+// tensor memory are another's (64 KB take microseconds; a copy whose barrier is the peer's cannot be waited for here).
+static __device__ __noinline__ void let_work_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
 // mbar_wait with the waiting part out of line: for kernels whose roles run side by side and would not stay in the
 // instruction cache with it at every wait.
 static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, int* status, volatile int* abort) {
