@@ -611,6 +611,9 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       float2 st[16];  // FP8: the tokens' scales
       if (kFp8) {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.sc_full[buf]), (i >> 1) & 1, p.status, abort)) && ok;
+        // log2 of the scales, a lane's token each (one nobody sees: its score is -inf, whatever its scale).  They set
+        // the reference alone, so the hardware's 2^-22 will do; log2f took a tile 200 cycles (this 40 to 140).
+        logs[lane] = (w >> lane & 1u) != 0 ? __log2f(reinterpret_cast<const float*>(sc)[buf * 2 * kPage + lane]) : 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float4 f = sc[buf * 2 * kPage / 4 + c];
@@ -624,8 +627,6 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (!(w >> (2 * c + 1) & 1u)) st[c].y = 0.f;
           }
         }
-        // log2 of the scales, a lane's token each (one nobody sees: its score is -inf, whatever its scale)
-        logs[lane] = (w >> lane & 1u) != 0 ? log2f(reinterpret_cast<const float*>(sc)[buf * 2 * kPage + lane]) : 0.f;
         __syncwarp();
       }
       ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&bars.s_full[buf]), (i >> 1) & 1, p.status, abort)) && ok;
