@@ -612,8 +612,10 @@ decode_masked_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (kFp8) {
         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars.sc_full[buf]), (i >> 1) & 1, p.status, abort)) && ok;
         // log2 of the scales, a lane's token each (one nobody sees: its score is -inf, whatever its scale).  They set
-        // the reference alone, so the hardware's 2^-22 will do; log2f took a tile 200 cycles (this 40 to 140).
-        logs[lane] = (w >> lane & 1u) != 0 ? __log2f(reinterpret_cast<const float*>(sc)[buf * 2 * kPage + lane]) : 0.f;
+        // the reference alone, so the hardware's 2^-22 will do; log2f took a tile 200 cycles (this 40 to 140).  A scale
+        // of 0 leaves a token its part of the sum, and the reference finite: 2^-96 keeps that sum in range.
+        const float s = reinterpret_cast<const float*>(sc)[buf * 2 * kPage + lane];
+        logs[lane] = (w >> lane & 1u) != 0 ? fmaxf(__log2f(s), -96.f) : 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float4 f = sc[buf * 2 * kPage / 4 + c];

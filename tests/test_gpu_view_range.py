@@ -39,11 +39,11 @@ def check(p, window=0, lse_tol=1.5e-3):
             o_ref, lse_ref = V.attend(f64(p.q[b])[:, HEADS], p.rows[b], seen[b])
             assert np.abs(f64(lse[b])[:, HEADS] - lse_ref).max() < lse_tol
             ref = np.einsum("nhm,hdm->nhd", o_ref, w)
-            err = np.linalg.norm(f64(out[b])[:, HEADS] - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
-            assert err.max() < 5e-3, (split, err)
+            err, size = np.linalg.norm(f64(out[b])[:, HEADS] - ref, axis=-1), np.linalg.norm(ref, axis=-1)
+            assert (err <= 5e-3 * size).all(), (split, err, size)
             if p.splits == 1:
-                err = np.linalg.norm(f64(latent[b])[:, HEADS] - o_ref, axis=-1) / np.linalg.norm(o_ref, axis=-1)
-                assert err.max() < 5e-3, err
+                err, size = np.linalg.norm(f64(latent[b])[:, HEADS] - o_ref, axis=-1), np.linalg.norm(o_ref, axis=-1)
+                assert (err <= 5e-3 * size).all(), (err, size)
 
 
 @pytest.mark.parametrize("shift", [0, 7, 9, 13, 16])
@@ -95,4 +95,27 @@ def test_a_query_whose_parts_differ_in_size(x):
     p.q[..., :512] *= 2.0 ** -x
     p.q[..., 512:] *= 2.0 ** x
     p.w_uv = (p.w_uv.float() * 2.0 ** -x).to(torch.bfloat16)
+    check(p)
+
+
+@pytest.mark.parametrize("zeros", [1, 64, 128, 300])
+def test_tokens_of_scale_zero_count_in_the_sum(zeros):
+    """A row of zeros with a scale of 0 is a token: score 0, value 0.  In front of the others, and alone."""
+    p = Problem([400, max(zeros - 2, 0)], 2, seed=zeros, fp8=True)
+    g = torch.Generator().manual_seed(zeros)
+    for b in range(p.B):
+        n = p.prior[b] + p.n_q
+        c, k = torch.randn(n, 512, generator=g), torch.randn(n, 64, generator=g)
+        s = c.abs().amax(1) / 448.0
+        none = torch.arange(n) < zeros
+        fill(p, b, torch.where(none[:, None], torch.zeros(()), c), torch.where(none[:, None], torch.zeros(()), k),
+             torch.where(none, torch.ones(()), s))
+        t = torch.arange(n)[none]
+        p.parts[1][p.table[b, t // PAGE].long(), t % PAGE] = 0.0
+    if zeros > 2:  # the second sequence holds nothing else: O' = 0, and the logarithm of the number of tokens
+        out, lse, latent = p.run(1 << 20)
+        n = torch.arange(1, 3) + p.prior[1]
+        assert not latent[1].any() and not out[1].any()
+        assert (lse[1].cpu() - n.float().log()[:, None]).abs().max() < 1e-5
+        p.prior, p.B, p.table, p.q, p.rows = p.prior[:1], 1, p.table[:1], p.q[:1], p.rows[:1]
     check(p)
