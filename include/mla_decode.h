@@ -602,8 +602,8 @@ mla_status mla_read_kv_fp8(const uint8_t* cache_c8, const float* cache_scale, co
  *   within 2^-3 and to nearest down to 2^-23, and within 2^-26 of the largest below that.
  * mla_masked_combine_out_absorb -- mla_combine_out_absorb for their partials, with O' in two
  *   bf16 parts (16 bits) instead of one; with a single split lse is already written.
- * MLA_ERR_UNSUPPORTED where 2 B n_q splits or 128 B n_q do not fit in 31 bits, or 64 num_pages
- * does not.
+ * MLA_ERR_UNSUPPORTED where 2 B n_q splits (as split_pages asks for them, before they are held
+ * to 64) or 128 B n_q do not fit in 31 bits, or 64 num_pages does not.
  *
  * mla_accept_tokens -- after a tree's step, the accepted path's rows moved together:
  *   for i < counts[b], slot seq_lens_before[b] + i takes the row of slot

@@ -36,23 +36,27 @@
 // The query: x1 = E4M3(x) and x2 = E4M3(x - x1), which holds a bf16 value without loss (its
 // rows scaled by a power of two, down to 2^-10 of the row's largest value).  P, whose small
 // weights count where there are many: x1 = E5M2(x) and x2 = E4M3(x - x1), with 2^9 at the row's
-// reference.  That is bf16's half a step, 2^-8 of a weight, down to 2^-11 of the row's largest,
-// and 2^-3 of it, to nearest, down to 2^-23 (0 below 2^-26).  With both parts in E4M3 and 64 at
-// the reference a weight was within 2^-9, but 0 below 2^-16: of 8191 tokens 12 nats below a
-// first one a quarter of the result was missing.  Codes take half the bytes of bf16 rows on the way and in shared memory, so three
-// buffers fit instead of two.  Widening them to f16 in front of the MMAs instead, by eight warps
-// of each CTA, took 6,700 cycles a tile: they waited for their own loads.
+// reference, the largest product of a weight and its token's scale.  That is bf16's half a step,
+// 2^-8 of a product, down to 2^-11 of the largest, and 2^-3 of it, to nearest, down to 2^-23 (0
+// below 2^-26).  With both parts in E4M3 and 64 at the reference a product was within 2^-9, but 0
+// below 2^-16: of 8191 tokens 12 nats below a first one a quarter of the result was missing.
+// Codes take half the bytes of bf16 rows on the way and in shared memory, so three buffers fit
+// instead of two.  Widening them to f16 in front of the MMAs instead, by eight warps of each CTA,
+// took 6,700 cycles a tile: they waited for their own loads.
 //
-// What bounds it: a tile's products take 2,284 cycles and read 360 KB of each CTA's shared memory
-// (2,812 cycles at 128 bytes a cycle); a tile takes 2,750 (FP8: 2,540).  32 sequences of 8192 tokens,
-// 32 queries each: 1400 us, 1.67 PFLOP/s; 16 of 2000-6000 with 24 over the FP8 cache: 326 us.  A
-// pair's fixed cost (launch, query, first tile, the way out) is some six tiles, and where units do not
-// fill their last wave of pairs the GPU waits for it: 96 queries of 2060 tokens 64 us, of which the
-// products are 31.  Sharing out all tiles evenly instead (pairs that go on from one unit to the next)
-// filled the waves, but its bookkeeping in every role cost 5-25% a tile, more than it gained on all
-// but a few sizes.
+// What bounds it: a tile's products take 2,284 cycles by themselves, a tile 2,680 (2,650 to 2,770 over
+// the units of 32 x 32 queries; FP8: 2,570 for a unit by itself, 2,780 on a full GPU), so the tensor cores
+// work 85% of the time.  What the other 15% wait for is not known: operands, loads and P move 360 KB
+// through each CTA's shared memory (240 + 104 + 16; 2,880 cycles if all of it went at 128 bytes a cycle,
+// which the measured tile shows it need not).  32 sequences of 8192 tokens, 32 queries each: 1420 us, 1.64
+// PFLOP/s; 16 of 2000-6000 with 24 over the FP8 cache: 339 us.  A pair's fixed cost (launch, query, first
+// tile, the way out) is some six tiles, and where units do not fill their last wave of pairs the GPU
+// waits for it: 96 queries of 2060 tokens 64 us, of which the products are 31.  Sharing out all tiles
+// evenly instead (pairs that go on from one unit to the next) filled the waves, but its bookkeeping in
+// every role cost 5-25% a tile, more than it gained on all but a few sizes.
 //
-// P is rounded to bf16, the type of the rows that it weighs; O' leaves in float32, as a split's partial too.
+// P is rounded to bf16, the type of the rows that it weighs (a second bf16 part would be 16 more products of 66
+// cycles a tile, and 16 KB of shared memory that the tiles fill); O' leaves in float32, as a split's partial too.
 //
 // Roles: warps 0-7 softmax (thread = one head and half a page of the tile); warp 8 loads keys,
 // warp 9 the RoPE keys, the values that replace keys, and scales; in CTA 0 warp 10 issues the

@@ -103,7 +103,7 @@ class DecodeSession:
         """``tree``: the parents [B, n_q] int32 of the drafted nodes (``mla_tree_prepare``), changed for later steps by
         :meth:`set_tree`.  ``window``, ``sinks``: the last and first tokens that a query sees (0: all).  Pages without a
         visible token need not be there, but for the non-absorbed path over the FP8 cache, which reads whole sequences
-        back."""
+        back.  That path's keys and values are laid out for ``max_kv_len`` tokens (64 KB each), whatever the window."""
         self.inp = inp
         self.cache_format = inp.workload.cache_format
         if self.cache_format not in ("bf16", "fp8"):
@@ -256,7 +256,9 @@ class DecodeSession:
 
     def accept(self, path: torch.Tensor, counts: torch.Tensor, stream=None):
         """After a tree's step: the rows of the accepted ``path`` [B, n_q] (``counts`` [B] nodes of it) move to the
-        first slots behind the context.  The lengths of the next step are the caller's."""
+        first slots behind the context.  The lengths of the next step are the caller's: ``kv_lens`` up to
+        ``max_kv_len``, the longest that the session was laid out for, and within the table's pages (a step with a longer
+        one reports MLA_ERR_BOUNDS in the device status and leaves that sequence zeros)."""
         if not self.tree:
             raise ValueError("only a tree's step has a path to accept")
         keep = ops.mla_accept_tokens_fp8 if self.cache_format == "fp8" else ops.mla_accept_tokens
