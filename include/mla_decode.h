@@ -597,9 +597,10 @@ mla_status mla_read_kv_fp8(const uint8_t* cache_c8, const float* cache_scale, co
  *   0 .. n_q - 1 sets MLA_ERR_BOUNDS and leaves zeros.
  * mla_decode_attn_masked_fp8_partial -- the same over the FP8 cache.  A head's latent query is
  *   taken in two E4M3 parts scaled by a power of two of its own (exact down to 2^-10 of its
- *   largest value), its rotated part in float16 by another, and P times a token's scale in an
- *   E5M2 and an E4M3 part: within 2^-8 of such a product down to 2^-11 of the row's largest,
- *   within 2^-3 and to nearest down to 2^-23, and within 2^-26 of the largest below that.
+ *   largest value, within 2^-17 of that below), its rotated part in float16 by another, and P
+ *   times a token's scale in an E5M2 and an E4M3 part: within 2^-8 of such a product down to
+ *   2^-11 of the row's largest, within 2^-3 and to nearest down to 2^-23, and within 2^-26 of
+ *   the largest below that.
  * mla_masked_combine_out_absorb -- mla_combine_out_absorb for their partials, with O' in two
  *   bf16 parts (16 bits) instead of one; with a single split lse is already written.
  * MLA_ERR_UNSUPPORTED where 2 B n_q splits (as split_pages asks for them, before they are held

@@ -34,7 +34,8 @@
 // The FP8 cache keeps this shape and multiplies the E4M3 codes as they are (kind::f8f6f4,
 // K = 32 at the same time as K = 16 of 16 bits), with the other operand in two 8-bit parts.
 // The query: x1 = E4M3(x) and x2 = E4M3(x - x1), which holds a bf16 value without loss (its
-// rows scaled by a power of two, down to 2^-10 of the row's largest value).  P, whose small
+// rows scaled by a power of two, down to 2^-10 of the row's largest value; E5M2 first would take
+// the range further, and a bit from every value).  P, whose small
 // weights count where there are many: x1 = E5M2(x) and x2 = E4M3(x - x1), with 2^9 at the row's
 // reference, the largest product of a weight and its token's scale.  That is bf16's half a step,
 // 2^-8 of a product, down to 2^-11 of the largest, and 2^-3 of it, to nearest, down to 2^-23 (0
